@@ -20,10 +20,13 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = range(5)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_EPI_NONE, MOE_EPI_SILU_MUL = 0, 1
+MOE_INT4, MOE_MXFP4 = 0, 1
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 I64 = ctypes.c_int64
+F32 = ctypes.c_float
+F64 = ctypes.c_double
 SZ = ctypes.c_size_t
 
 
@@ -57,6 +60,16 @@ SIGNATURES: dict[str, tuple] = {
     "moe_backward_workspace": (SZ, [I64, I64, I64, I32, I32, I32]),
     "moe_backward": (I32, [P, P, P, P, P, I32, I64, I64, I64, I32, I32, P, P, P, P, P, P, P, P, I32, P, P,
                            SZ, P]),
+    "moe_quantize_fourbit": (I32, [P, I32, I32, I64, I64, I32, I32, P, P, P]),
+    "moe_grouped_matvec_fourbit": (I32, [P, I64, P, I32, P, P, I32, I32, P, I32, I64, I64, I64, I32, P, I32, P]),
+    "moe_forward_fourbit_workspace": (SZ, [I64, I64, I64, I32, I32]),
+    "moe_forward_fourbit": (I32, [P, P, P, P, P, P, I32, I32, I64, I64, I64, I32, I32, I64, I32, P, I32,
+                                  ctypes.POINTER(MoeAux), P, SZ, P]),
+    "moe_layer_norm": (I32, [P, I32, I64, I64, P, P, I32, F32, I32, P, P, P, P]),
+    "moe_layer_norm_backward_workspace": (SZ, [I64, I64]),
+    "moe_layer_norm_backward": (I32, [P, P, I32, I64, I64, P, I32, P, P, I32, P, P, P, I32, P, SZ, P]),
+    "moe_dropout_add": (I32, [P, I32, P, I32, I64, F64, P, P, I32, P]),
+    "moe_unpermute_combine_dropout": (I32, [P, I32, P, P, P, I32, I64, I64, I32, P, I32, F64, P, P, I32, P]),
     "moe_status_string": (ctypes.c_char_p, [I32]),
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_abi_version": (I32, []),
@@ -79,6 +92,15 @@ class MoeKernels:
     forward: Callable
     backward_workspace: Callable
     backward: Callable
+    quantize_fourbit: Callable
+    grouped_matvec_fourbit: Callable
+    forward_fourbit_workspace: Callable
+    forward_fourbit: Callable
+    layer_norm: Callable
+    layer_norm_backward_workspace: Callable
+    layer_norm_backward: Callable
+    dropout_add: Callable
+    unpermute_combine_dropout: Callable
     status_string: Callable
     last_error: Callable
     abi_version: Callable

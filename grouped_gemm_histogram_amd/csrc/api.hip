@@ -5,6 +5,7 @@
 // and keeps no pointer.  Errors come back as moe_status_t plus a thread-local
 // message; no C++ exception crosses the boundary.
 
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -282,6 +283,79 @@ moe_status_t grouped_gemm_impl(const void* A, const float* a_scales, long long A
   return launched(moe::launch_grouped_gemm(p, as_stream(stream)), "grouped_gemm");
 }
 
+moe_status_t check_combine(const void* y, moe_dtype_t y_dtype, const int32_t* row_pos, const float* topk_weights,
+                           const int32_t* offsets, int32_t E, int64_t T, int64_t H, int32_t k, const void* out,
+                           moe_dtype_t out_dtype) {
+  if (moe_status_t s = check_experts(E, k)) return s;
+  MOE_REQUIRE(T >= 0 && T * k <= kMaxRows && H > 0 && H <= kMaxRows, "bad sizes");
+  MOE_REQUIRE(y_dtype == MOE_F32 || y_dtype == MOE_BF16, "y_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(out_dtype == MOE_F32 || out_dtype == MOE_BF16, "out_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE((H * esize(y_dtype)) % 16 == 0 && H % 4 == 0, "rows of y must be a multiple of 16 bytes");
+  if (T == 0) return MOE_OK;
+  MOE_REQUIRE(y && row_pos && topk_weights && offsets && out, "null pointer argument");
+  MOE_REQUIRE(aligned16(y) && aligned16(out), "y and out must be 16-byte aligned");
+  return MOE_OK;
+}
+
+// The forward's routing arrays, in the workspace or the caller's.
+struct Routing {
+  int32_t* ids;
+  float* weights;
+  int32_t *offsets, *sorted, *rowpos;
+};
+
+// Records stage event i, when the caller gave it.
+struct StageEvents {
+  void** ev;
+  void* stream;
+  moe_status_t operator()(int i) const {
+    if (ev && ev[i] && hipEventRecord(static_cast<hipEvent_t>(ev[i]), as_stream(stream)) != hipSuccess)
+      return fail(MOE_ERR_LAUNCH, "hipEventRecord of stage event %d failed", i);
+    return MOE_OK;
+  }
+};
+
+// The first two stages of a layer forward, routing and offsets, with stage events 0 to 2.
+moe_status_t route_stages(const float* router_logits, int64_t T, int32_t E, int32_t k, int64_t num_valid_rows,
+                          int32_t renormalize, const Routing& r, void* offws, const StageEvents& mark,
+                          void* stream) {
+  const long long R = T * k;
+  moe_status_t s;
+  if ((s = mark(0))) return s;
+  if (R > 0 && R <= 1024 && T <= 16) {
+    // decode sizes: routing and offsets in one launch, a wave per token (the offsets
+    // stage's events then enclose no work).  With more tokens than the workgroup's 16
+    // waves the waves route several tokens one after another, which measured slower
+    // than the separate routing launch (T = 64: +9 us; T = 1 and 8: -1 and -3 us).
+    if ((s = launched(moe::launch_route_offsets_single(router_logits, (int)T, E, k, num_valid_rows,
+                                                       renormalize ? 1 : 0, r.ids, r.weights, r.offsets, r.sorted, r.rowpos,
+                                                       as_stream(stream)),
+                      "route_offsets_single")))
+      return s;
+    if ((s = mark(1))) return s;
+  } else if (T > 0) {
+    // routing with the per-chunk histograms (the routing stage), then the per-bin scan
+    // over chunks and the scatter (the offsets stage)
+    if ((s = launched(moe::launch_route_hist(router_logits, (int)T, E, k, num_valid_rows, renormalize ? 1 : 0,
+                                             r.ids, r.weights, offws, as_stream(stream)),
+                      "route_hist")))
+      return s;
+    if ((s = mark(1))) return s;
+    if ((s = launched(moe::launch_offsets_from_hist(r.ids, (int)T, E, k, r.offsets, r.sorted, r.rowpos, offws,
+                                                    as_stream(stream)),
+                      "offsets_from_hist")))
+      return s;
+  } else {
+    if ((s = moe_route_topk(router_logits, T, E, k, num_valid_rows, renormalize, r.ids, r.weights, stream)))
+      return s;
+    if ((s = mark(1))) return s;
+    if ((s = moe_build_offsets(r.ids, R, E, r.offsets, r.sorted, r.rowpos, offws,
+                               moe::build_offsets_workspace_bytes(R, E), stream)))
+      return s;
+  }
+  return mark(2);
+}
+
 }  // namespace
 
 extern "C" {
@@ -337,14 +411,8 @@ moe_status_t moe_unpermute_combine(const void* y, moe_dtype_t y_dtype, const int
                                    const float* topk_weights, const int32_t* offsets, int32_t E,
                                    int64_t T, int64_t H, int32_t k, void* out,
                                    moe_dtype_t out_dtype, void* stream) {
-  if (moe_status_t s = check_experts(E, k)) return s;
-  MOE_REQUIRE(T >= 0 && T * k <= kMaxRows && H > 0 && H <= kMaxRows, "bad sizes");
-  MOE_REQUIRE(y_dtype == MOE_F32 || y_dtype == MOE_BF16, "y_dtype must be MOE_F32 or MOE_BF16");
-  MOE_REQUIRE(out_dtype == MOE_F32 || out_dtype == MOE_BF16, "out_dtype must be MOE_F32 or MOE_BF16");
-  MOE_REQUIRE((H * esize(y_dtype)) % 16 == 0 && H % 4 == 0, "rows of y must be a multiple of 16 bytes");
+  if (moe_status_t s = check_combine(y, y_dtype, row_pos, topk_weights, offsets, E, T, H, k, out, out_dtype)) return s;
   if (T == 0) return ok();
-  MOE_REQUIRE(y && row_pos && topk_weights && offsets && out, "null pointer argument");
-  MOE_REQUIRE(aligned16(y) && aligned16(out), "y and out must be 16-byte aligned");
   return launched(moe::launch_combine(y, y_dtype == MOE_BF16, row_pos, topk_weights, offsets, E, (int)T,
                                       (int)H, k, out, out_dtype == MOE_BF16, as_stream(stream)),
                   "unpermute_combine");
@@ -389,47 +457,11 @@ moe_status_t moe_forward(const void* x, moe_dtype_t x_dtype, const float* router
   int32_t* sorted = (aux && aux->sorted_rows) ? aux->sorted_rows : reinterpret_cast<int32_t*>(ws + L.sorted);
   int32_t* rowpos = (aux && aux->row_pos) ? aux->row_pos : reinterpret_cast<int32_t*>(ws + L.rowpos);
   const long long R = T * k;
-  void** ev = aux ? aux->stage_events : nullptr;
-  auto mark = [&](int i) -> moe_status_t {
-    if (ev && ev[i] && hipEventRecord(static_cast<hipEvent_t>(ev[i]), as_stream(stream)) != hipSuccess)
-      return fail(MOE_ERR_LAUNCH, "hipEventRecord of stage event %d failed", i);
-    return MOE_OK;
-  };
+  const StageEvents mark{aux ? aux->stage_events : nullptr, stream};
 
   moe_status_t s;
-  if ((s = mark(0))) return s;
-  if (R > 0 && R <= 1024 && T <= 16) {
-    // decode sizes: routing and offsets in one launch, a wave per token (the offsets
-    // stage's events then enclose no work).  With more tokens than the workgroup's 16
-    // waves the waves route several tokens one after another, which measured slower
-    // than the separate routing launch (T = 64: +9 us; T = 1 and 8: -1 and -3 us).
-    if ((s = launched(moe::launch_route_offsets_single(router_logits, (int)T, E, k, num_valid_rows,
-                                                       renormalize ? 1 : 0, ids, wts, offs, sorted, rowpos,
-                                                       as_stream(stream)),
-                      "route_offsets_single")))
-      return s;
-    if ((s = mark(1))) return s;
-  } else if (T > 0) {
-    // routing with the per-chunk histograms (the routing stage), then the per-bin scan
-    // over chunks and the scatter (the offsets stage)
-    if ((s = launched(moe::launch_route_hist(router_logits, (int)T, E, k, num_valid_rows, renormalize ? 1 : 0,
-                                             ids, wts, ws + L.offws, as_stream(stream)),
-                      "route_hist")))
-      return s;
-    if ((s = mark(1))) return s;
-    if ((s = launched(moe::launch_offsets_from_hist(ids, (int)T, E, k, offs, sorted, rowpos, ws + L.offws,
-                                                    as_stream(stream)),
-                      "offsets_from_hist")))
-      return s;
-  } else {
-    if ((s = moe_route_topk(router_logits, T, E, k, num_valid_rows, renormalize, ids, wts, stream)))
-      return s;
-    if ((s = mark(1))) return s;
-    if ((s = moe_build_offsets(ids, R, E, offs, sorted, rowpos, ws + L.offws,
-                               moe::build_offsets_workspace_bytes(R, E), stream)))
-      return s;
-  }
-  if ((s = mark(2))) return s;
+  const Routing r{ids, wts, offs, sorted, rowpos};
+  if ((s = route_stages(router_logits, T, E, k, num_valid_rows, renormalize, r, ws + L.offws, mark, stream))) return s;
   if (T == 0) {
     for (int i = 3; i <= MOE_FORWARD_STAGES; ++i)
       if ((s = mark(i))) return s;
@@ -688,4 +720,294 @@ moe_status_t moe_backward(const void* x, const void* w13, const float* w13_scale
   return launched(e, "backward");
 }
 
-}  // extern "C\"
+}  // extern "C"
+
+// ------------------------------------------------------------------------- 4-bit weights
+
+namespace {
+
+moe_status_t check_fourbit(moe_fourbit_t format, int32_t group, int64_t K) {
+  MOE_REQUIRE(format == MOE_INT4 || format == MOE_MXFP4, "format must be MOE_INT4 or MOE_MXFP4");
+  if (format == MOE_MXFP4)
+    MOE_REQUIRE(group == 32, "mxfp4 groups have 32 channels, not %d", group);
+  else
+    MOE_REQUIRE(group == 32 || group == 64 || group == 128, "int4 groups have 32, 64 or 128 channels, not %d", group);
+  MOE_REQUIRE(K > 0 && K % group == 0, "K=%lld is not a multiple of group=%d", (long long)K, group);
+  return MOE_OK;
+}
+
+struct FourbitLayout {
+  size_t ids, w, offsets, sorted, rowpos, offws, h, y, total;
+};
+
+FourbitLayout fourbit_layout(long long T, long long H, long long I, int E, int k) {
+  const long long R = T * k;
+  FourbitLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.ids = take(R * 4);
+  L.w = take(R * 4);
+  L.offsets = take((E + 1) * 4);
+  L.sorted = take(R * 4);
+  L.rowpos = take(R * 4);
+  L.offws = take(std::max(moe::build_offsets_workspace_bytes(R, E), moe::route_offsets_workspace_bytes(T, E)));
+  L.h = take(R * I * 2);
+  L.y = take(R * H * 2);
+  L.total = off;
+  return L;
+}
+
+bool fourbit_sizes_ok(long long T, long long H, long long I, int E, int k) {
+  return E >= 1 && E <= MOE_MAX_EXPERTS && k >= 1 && k <= MOE_MAX_TOPK && k <= E && T >= 0 && H > 0 && I > 0 &&
+         H <= kMaxRows && 2 * I <= kMaxRows && T <= kMaxRows && T * k <= kMaxRows;
+}
+
+// a launch's grid has 256-thread workgroups and under 2^32 threads
+constexpr long long kMaxWorkgroups = (1ll << 24) - 1;
+
+moe_status_t check_dropout(double p, const uint64_t* rng) {
+  MOE_REQUIRE(p >= 0.0 && p <= 1.0, "p=%g outside [0, 1]", p);
+  MOE_REQUIRE(rng, "rng is null");
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(rng) & 7u) == 0, "rng must be 8-byte aligned");
+  return MOE_OK;
+}
+
+// bytes [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void* a, long long na, const void* b, long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+bool f32_or_bf16(int d) { return d == MOE_F32 || d == MOE_BF16; }
+
+bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E, int64_t N, int64_t K,
+                                  moe_fourbit_t format, int32_t group, void* codes, void* scales, void* stream) {
+  MOE_REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "E=%d outside [1, %d]", E, MOE_MAX_EXPERTS);
+  MOE_REQUIRE(f32_or_bf16(w_dtype), "w_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(N > 0 && N <= kMaxRows && K > 0 && K <= kMaxRows, "bad sizes");
+  if (moe_status_t s = check_fourbit(format, group, K)) return s;
+  MOE_REQUIRE(N * K <= (1ll << 34) / E, "E*N*K exceeds 2^34");
+  MOE_REQUIRE(w && codes && scales, "null pointer argument");
+  MOE_REQUIRE(aligned16(w) && aligned16(codes) && aligned16(scales), "w, codes and scales must be 16-byte aligned");
+  return launched(moe::launch_quantize_fourbit(w, w_dtype == MOE_BF16, E * N * K, format == MOE_INT4, group, codes,
+                                               scales, as_stream(stream)),
+                  "quantize_fourbit");
+}
+
+moe_status_t moe_grouped_matvec_fourbit(const void* A, int64_t A_rows, const int32_t* gather_rows,
+                                        int32_t gather_div, const void* codes, const void* scales,
+                                        moe_fourbit_t format, int32_t group, const int32_t* offsets, int32_t E,
+                                        int64_t M_rows, int64_t N, int64_t K, moe_epilogue_t epi, void* C,
+                                        moe_dtype_t c_dtype, void* stream) {
+  MOE_REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "E=%d outside [1, %d]", E, MOE_MAX_EXPERTS);
+  MOE_REQUIRE(epi == MOE_EPI_NONE || epi == MOE_EPI_SILU_MUL, "bad epilogue");
+  MOE_REQUIRE(f32_or_bf16(c_dtype), "c_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(M_rows >= 0 && M_rows <= kMaxRows && A_rows >= 0 && A_rows <= kMaxRows && N > 0 && N <= kMaxRows &&
+                  K > 0 && K <= kMaxRows,
+              "bad sizes");
+  if (moe_status_t s = check_fourbit(format, group, K)) return s;
+  const bool silu = epi == MOE_EPI_SILU_MUL;
+  MOE_REQUIRE(!silu || N % 2 == 0, "SiLU*up needs an even N");
+  if (gather_rows)
+    MOE_REQUIRE(gather_div >= 1 && gather_div <= MOE_MAX_TOPK, "gather_div=%d outside [1, %d]", gather_div,
+                MOE_MAX_TOPK);
+  else
+    MOE_REQUIRE(A_rows >= M_rows, "A has %lld rows but the product has %lld", (long long)A_rows, (long long)M_rows);
+  if (M_rows == 0) return ok();
+  MOE_REQUIRE(A_rows > 0, "A has no rows but the product has %lld", (long long)M_rows);
+  MOE_REQUIRE(A && codes && scales && offsets && C, "null pointer argument");
+  MOE_REQUIRE(aligned16(A) && aligned16(codes) && aligned16(scales) && aligned16(C),
+              "A, codes, scales and C must be 16-byte aligned");
+  if (moe::fourbit_workgroups(M_rows, E, silu ? N / 2 : N) > kMaxWorkgroups)
+    return fail(MOE_ERR_UNSUPPORTED, "%lld rows of %lld columns exceed one launch", (long long)M_rows, (long long)N);
+  moe::FourbitLaunch p{};
+  p.A = A;
+  p.a_rows = gather_rows;
+  p.a_div = gather_div;
+  p.a_total = A_rows;
+  p.codes = codes;
+  p.scales = scales;
+  p.int4 = format == MOE_INT4;
+  p.group = group;
+  p.offsets = offsets;
+  p.E = E;
+  p.M_rows = M_rows;
+  p.N = N;
+  p.K = K;
+  p.silu = silu;
+  p.C = C;
+  p.c_f32 = c_dtype == MOE_F32;
+  return launched(moe::launch_fourbit(p, as_stream(stream)), "grouped_matvec_fourbit");
+}
+
+size_t moe_forward_fourbit_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+  if (!fourbit_sizes_ok(T, H, I, E, k)) return 0;
+  return fourbit_layout(T, H, I, E, k).total;
+}
+
+moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, const void* w13_codes,
+                                 const void* w13_scales, const void* w2_codes, const void* w2_scales,
+                                 moe_fourbit_t format, int32_t group, int64_t T, int64_t H, int64_t I, int32_t E,
+                                 int32_t k, int64_t num_valid_rows, int32_t renormalize, void* out,
+                                 moe_dtype_t out_dtype, moe_aux_t* aux, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (moe_status_t s = check_experts(E, k)) return s;
+  MOE_REQUIRE(fourbit_sizes_ok(T, H, I, E, k), "bad sizes");
+  if (moe_status_t s = check_fourbit(format, group, H)) return s;
+  if (moe_status_t s = check_fourbit(format, group, I)) return s;
+  MOE_REQUIRE(f32_or_bf16(out_dtype), "out_dtype must be MOE_F32 or MOE_BF16");
+  const long long R = T * k;
+  if (T > 0) {
+    MOE_REQUIRE(x && router_logits && w13_codes && w13_scales && w2_codes && w2_scales && out,
+                "null pointer argument");
+    MOE_REQUIRE(aligned16(x) && aligned16(w13_codes) && aligned16(w13_scales) && aligned16(w2_codes) &&
+                    aligned16(w2_scales) && aligned16(out),
+                "x, weights, scales and out must be 16-byte aligned");
+    if (std::max(moe::fourbit_workgroups(R, E, I), moe::fourbit_workgroups(R, E, H)) > kMaxWorkgroups)
+      return fail(MOE_ERR_UNSUPPORTED, "%lld routed rows exceed one launch", R);
+  }
+  const FourbitLayout L = fourbit_layout(T, H, I, E, k);
+  if (!workspace || workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, L.total);
+  MOE_REQUIRE(aligned16(workspace), "workspace must be 16-byte aligned");
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const Routing r{(aux && aux->topk_ids) ? aux->topk_ids : reinterpret_cast<int32_t*>(ws + L.ids),
+                  (aux && aux->topk_weights) ? aux->topk_weights : reinterpret_cast<float*>(ws + L.w),
+                  (aux && aux->offsets) ? aux->offsets : reinterpret_cast<int32_t*>(ws + L.offsets),
+                  (aux && aux->sorted_rows) ? aux->sorted_rows : reinterpret_cast<int32_t*>(ws + L.sorted),
+                  (aux && aux->row_pos) ? aux->row_pos : reinterpret_cast<int32_t*>(ws + L.rowpos)};
+  const StageEvents mark{aux ? aux->stage_events : nullptr, stream};
+  moe_status_t s;
+  if ((s = route_stages(router_logits, T, E, k, num_valid_rows, renormalize, r, ws + L.offws, mark, stream))) return s;
+  if (T == 0) {
+    for (int i = 3; i <= MOE_FORWARD_STAGES; ++i)
+      if ((s = mark(i))) return s;
+    return ok();
+  }
+  if ((s = mark(3))) return s;
+  if ((s = moe_grouped_matvec_fourbit(x, T, r.sorted, k, w13_codes, w13_scales, format, group, r.offsets, E, R, 2 * I,
+                                      H, MOE_EPI_SILU_MUL, ws + L.h, MOE_BF16, stream)))
+    return s;
+  if ((s = mark(4))) return s;
+  if ((s = moe_grouped_matvec_fourbit(ws + L.h, R, nullptr, 1, w2_codes, w2_scales, format, group, r.offsets, E, R, H,
+                                      I, MOE_EPI_NONE, ws + L.y, MOE_BF16, stream)))
+    return s;
+  if ((s = mark(5))) return s;
+  if ((s = moe_unpermute_combine(ws + L.y, MOE_BF16, r.rowpos, r.weights, r.offsets, E, T, H, k, out, out_dtype,
+                                 stream)))
+    return s;
+  if ((s = mark(6))) return s;
+  return ok();
+}
+
+// ------------------------------------------------------------------------- norm and dropout
+
+moe_status_t moe_layer_norm(const void* x, moe_dtype_t x_dtype, int64_t T, int64_t H, const void* weight,
+                            const void* bias, moe_dtype_t w_dtype, float eps, int32_t rms, void* y, float* mean,
+                            float* rstd, void* stream) {
+  MOE_REQUIRE(f32_or_bf16(x_dtype), "x_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(f32_or_bf16(w_dtype), "w_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(T >= 0 && T <= kMaxRows && H > 0, "bad sizes");
+  if (H > moe::kNormMaxH)
+    return fail(MOE_ERR_UNSUPPORTED, "H=%lld exceeds %lld", (long long)H, (long long)moe::kNormMaxH);
+  MOE_REQUIRE(eps >= 0.0f && eps < INFINITY, "eps must be finite and >= 0");
+  if (T == 0) return ok();
+  MOE_REQUIRE(x && y, "null pointer argument");
+  MOE_REQUIRE(aligned16(x) && aligned16(y), "x and y must be 16-byte aligned");
+  MOE_REQUIRE(aligned_to(weight, esize(w_dtype)) && aligned_to(bias, esize(w_dtype)) && aligned_to(mean, 4) &&
+                  aligned_to(rstd, 4),
+              "weight, bias, mean and rstd must be aligned to their elements");
+  const long long bytes = T * H * esize(x_dtype);
+  MOE_REQUIRE(y == x || !overlap(x, bytes, y, bytes), "y overlaps x without being x");
+  moe::NormLaunch p{x, x_dtype == MOE_BF16, T, (int)H, weight, bias, w_dtype == MOE_BF16, eps, rms != 0, y, mean,
+                    rstd};
+  return launched(moe::launch_norm(p, as_stream(stream)), "layer_norm");
+}
+
+size_t moe_layer_norm_backward_workspace(int64_t T, int64_t H) {
+  if (T < 0 || T > kMaxRows || H <= 0 || H > moe::kNormMaxH) return 0;
+  return moe::norm_backward_workspace_bytes(T, (int)H);
+}
+
+moe_status_t moe_layer_norm_backward(const void* dy, const void* x, moe_dtype_t x_dtype, int64_t T, int64_t H,
+                                     const void* weight, moe_dtype_t w_dtype, const float* mean,
+                                     const float* rstd, int32_t rms, void* dx, void* dweight, void* dbias,
+                                     moe_dtype_t grad_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  MOE_REQUIRE(f32_or_bf16(x_dtype), "x_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(f32_or_bf16(w_dtype), "w_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(f32_or_bf16(grad_dtype), "grad_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(T >= 0 && T <= kMaxRows && H > 0, "bad sizes");
+  if (H > moe::kNormMaxH)
+    return fail(MOE_ERR_UNSUPPORTED, "H=%lld exceeds %lld", (long long)H, (long long)moe::kNormMaxH);
+  MOE_REQUIRE(aligned_to(weight, esize(w_dtype)) && aligned_to(mean, 4) && aligned_to(rstd, 4) &&
+                  aligned_to(dweight, esize(grad_dtype)) && aligned_to(dbias, esize(grad_dtype)),
+              "weight, mean, rstd, dweight and dbias must be aligned to their elements");
+  moe::NormBackwardLaunch p{dy, x, x_dtype == MOE_BF16, T, (int)H, weight, w_dtype == MOE_BF16, mean, rstd,
+                            rms != 0, dx, dweight, dbias, grad_dtype == MOE_BF16, nullptr};
+  if (T > 0) {
+    MOE_REQUIRE(dy && x && dx && rstd && (mean || rms), "null pointer argument");
+    MOE_REQUIRE(aligned16(dy) && aligned16(x) && aligned16(dx), "dy, x and dx must be 16-byte aligned");
+    const long long bytes = T * H * esize(x_dtype);
+    MOE_REQUIRE((dx == dy || !overlap(dy, bytes, dx, bytes)) && (dx == x || !overlap(x, bytes, dx, bytes)),
+                "dx overlaps dy or x without being it");
+    if (dweight || dbias) {
+      const size_t need = moe::norm_backward_workspace_bytes(T, (int)H);
+      if (!workspace || workspace_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+      MOE_REQUIRE(aligned16(workspace), "workspace must be 16-byte aligned");
+      p.part = static_cast<float*>(workspace);
+    }
+  }
+  return launched(moe::launch_norm_backward(p, as_stream(stream)), "layer_norm_backward");
+}
+
+moe_status_t moe_dropout_add(const void* x, moe_dtype_t x_dtype, const void* residual,
+                             moe_dtype_t residual_dtype, int64_t n, double p, const uint64_t* rng, void* out,
+                             moe_dtype_t out_dtype, void* stream) {
+  MOE_REQUIRE(f32_or_bf16(x_dtype) && f32_or_bf16(out_dtype) && (!residual || f32_or_bf16(residual_dtype)),
+              "x, residual and out must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(n >= 0 && n <= (1ll << 60), "n=%lld out of range", (long long)n);
+  if (moe_status_t s = check_dropout(p, rng)) return s;
+  if (n == 0) return ok();
+  MOE_REQUIRE(x && out, "null pointer argument");
+  MOE_REQUIRE(aligned16(x) && aligned16(out) && aligned16(residual), "x, residual and out must be 16-byte aligned");
+  auto clear = [&](const void* in, moe_dtype_t dt) {   // out is this input, or apart from it
+    return (in == out && dt == out_dtype) || !overlap(in, n * esize(dt), out, n * esize(out_dtype));
+  };
+  MOE_REQUIRE(clear(x, x_dtype) && (!residual || clear(residual, residual_dtype)),
+              "out overlaps x or residual without being it");
+  moe::DropoutLaunch d{x, x_dtype == MOE_BF16, residual, residual_dtype == MOE_BF16, n, p, rng, out,
+                       out_dtype == MOE_BF16};
+  return launched(moe::launch_dropout_add(d, as_stream(stream)), "dropout_add");
+}
+
+moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, const int32_t* row_pos,
+                                           const float* topk_weights, const int32_t* offsets, int32_t E,
+                                           int64_t T, int64_t H, int32_t k, const void* residual,
+                                           moe_dtype_t residual_dtype, double p, const uint64_t* rng, void* out,
+                                           moe_dtype_t out_dtype, void* stream) {
+  if (moe_status_t s = check_combine(y, y_dtype, row_pos, topk_weights, offsets, E, T, H, k, out, out_dtype)) return s;
+  MOE_REQUIRE(!residual || f32_or_bf16(residual_dtype), "residual_dtype must be MOE_F32 or MOE_BF16");
+  if (moe_status_t s = check_dropout(p, rng)) return s;
+  if (T == 0) return ok();
+  MOE_REQUIRE(aligned16(residual), "residual must be 16-byte aligned");
+  MOE_REQUIRE(!residual || !overlap(residual, T * H * esize(residual_dtype), out, T * H * esize(out_dtype)),
+              "out overlaps residual");
+  const moe::DropoutArgs drop{residual, residual_dtype == MOE_BF16, p, rng};
+  return launched(moe::launch_combine_dropout(y, y_dtype == MOE_BF16, row_pos, topk_weights, offsets, E, (int)T,
+                                              (int)H, k, drop, out, out_dtype == MOE_BF16, as_stream(stream)),
+                  "unpermute_combine_dropout");
+}
+
+}  // extern "C"

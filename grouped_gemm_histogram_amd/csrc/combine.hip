@@ -11,7 +11,7 @@
 
 #include <algorithm>
 
-#include "device_common.h"
+#include "dropout_device.h"
 #include "launch.h"
 #include "moe.h"
 
@@ -22,13 +22,20 @@ __device__ __forceinline__ void load16(const float* p, float* v) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
 }
 
-template <bool kBf16In, bool kBf16Out, int kUnroll>
+// dropout of the sum (kDrop >= 1) and the residual it is added to: none (1), f32 (2), bf16 (3)
+struct CombineDrop {
+  Drop d;
+  const uint64_t* rng;
+  const void* residual;
+};
+
+template <bool kBf16In, bool kBf16Out, int kUnroll, int kDrop>
 __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y_,
                                                       const int* __restrict__ row_pos,
                                                       const float* __restrict__ weights,
                                                       const int* __restrict__ offsets, int E, int T,
                                                       int H, int k, int nsplit, int cols,
-                                                      void* __restrict__ out_) {
+                                                      void* __restrict__ out_, CombineDrop drop) {
   // Elements per lane per step: 8 for bf16 input (one 16-B load), 4 for f32.
   constexpr int EL = kBf16In ? 8 : 4;
   const int wv = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -71,7 +78,36 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
       load16(static_cast<const float*>(y_) + (size_t)p * H + c0, v);
     }
   };
-  auto store_out = [&](int c0, const float (&acc)[EL]) {
+  uint64_t seed = 0, rng_offset = 0;
+  if constexpr (kDrop > 0) {
+    seed = drop.rng[0];
+    rng_offset = drop.rng[1];
+  }
+  auto store_out = [&](int c0, float (&acc)[EL]) {
+    if constexpr (kDrop > 0) {
+      // the lane's elements lie in one counter block: EL divides H and 8
+      const uint64_t at = (uint64_t)t * H + c0;
+      const uint32_t keep = keep_bits(rng_offset + (at >> 3), seed, drop.d) >> (at & 7);
+      float r[EL] = {};
+      if constexpr (kDrop == 2) {
+#pragma unroll
+        for (int i = 0; i < EL; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(drop.residual) + at + i);
+          r[i] = f.x; r[i + 1] = f.y; r[i + 2] = f.z; r[i + 3] = f.w;
+        }
+      } else if constexpr (kDrop == 3) {
+#pragma unroll
+        for (int i = 0; i < EL; i += 4) {
+          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(drop.residual) + at + i);
+          r[i] = bf16_bits_to_f32(u.x & 0xffffu);
+          r[i + 1] = bf16_bits_to_f32(u.x >> 16);
+          r[i + 2] = bf16_bits_to_f32(u.y & 0xffffu);
+          r[i + 3] = bf16_bits_to_f32(u.y >> 16);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < EL; ++i) acc[i] = (keep >> i & 1) ? fmaf(acc[i], drop.d.scale, r[i]) : r[i];
+    }
     if constexpr (kBf16Out) {
       uint16_t* o = static_cast<uint16_t*>(out_) + (size_t)t * H + c0;
       if constexpr (EL == 8) {
@@ -115,9 +151,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
   }
 }
 
-hipError_t launch_combine(const void* y, bool y_bf16, const int* row_pos, const float* weights,
-                          const int* offsets, int E, int T, int H, int k, void* out, bool out_bf16,
-                          hipStream_t stream) {
+template <int kDrop>
+static hipError_t launch_combine_t(const void* y, bool y_bf16, const int* row_pos, const float* weights,
+                                   const int* offsets, int E, int T, int H, int k, const CombineDrop& drop, void* out,
+                                   bool out_bf16, hipStream_t stream) {
   if (T <= 0) return hipSuccess;
   // few tokens: split each row over up to ceil(1024 / T) waves of whole 64-lane steps
   const int step = kWave * (y_bf16 ? 8 : 4);
@@ -133,11 +170,11 @@ hipError_t launch_combine(const void* y, bool y_bf16, const int* row_pos, const 
   const bool wide = (long long)T * k * H * (y_bf16 ? 2 : 4) > (256ll << 20);
 #define MOE_COMBINE_LAUNCH(BI, BO)                                                                   \
   if (wide)                                                                                           \
-    hipLaunchKernelGGL((combine_kernel<BI, BO, 4>), grid, block, 0, stream, y, row_pos, weights,     \
-                       offsets, E, T, H, k, nsplit, cols, out);                                       \
+    hipLaunchKernelGGL((combine_kernel<BI, BO, 4, kDrop>), grid, block, 0, stream, y, row_pos, weights,     \
+                       offsets, E, T, H, k, nsplit, cols, out, drop);                                      \
   else                                                                                                \
-    hipLaunchKernelGGL((combine_kernel<BI, BO, 2>), grid, block, 0, stream, y, row_pos, weights,     \
-                       offsets, E, T, H, k, nsplit, cols, out);
+    hipLaunchKernelGGL((combine_kernel<BI, BO, 2, kDrop>), grid, block, 0, stream, y, row_pos, weights,     \
+                       offsets, E, T, H, k, nsplit, cols, out, drop);
   if (y_bf16 && out_bf16) {
     MOE_COMBINE_LAUNCH(true, true)
   } else if (y_bf16) {
@@ -149,6 +186,23 @@ hipError_t launch_combine(const void* y, bool y_bf16, const int* row_pos, const 
   }
 #undef MOE_COMBINE_LAUNCH
   return hipGetLastError();
+}
+
+hipError_t launch_combine(const void* y, bool y_bf16, const int* row_pos, const float* weights,
+                          const int* offsets, int E, int T, int H, int k, void* out, bool out_bf16,
+                          hipStream_t stream) {
+  return launch_combine_t<0>(y, y_bf16, row_pos, weights, offsets, E, T, H, k, CombineDrop{}, out, out_bf16, stream);
+}
+
+hipError_t launch_combine_dropout(const void* y, bool y_bf16, const int* row_pos, const float* weights,
+                                  const int* offsets, int E, int T, int H, int k, const DropoutArgs& drop, void* out,
+                                  bool out_bf16, hipStream_t stream) {
+  const CombineDrop d{make_drop(drop.p), drop.rng, drop.residual};
+  if (!drop.residual)
+    return launch_combine_t<1>(y, y_bf16, row_pos, weights, offsets, E, T, H, k, d, out, out_bf16, stream);
+  if (!drop.residual_bf16)
+    return launch_combine_t<2>(y, y_bf16, row_pos, weights, offsets, E, T, H, k, d, out, out_bf16, stream);
+  return launch_combine_t<3>(y, y_bf16, row_pos, weights, offsets, E, T, H, k, d, out, out_bf16, stream);
 }
 
 }  // namespace moe

@@ -112,4 +112,85 @@ hipError_t launch_combine(const void* y, bool y_bf16, const int* row_pos, const 
                           const int* offsets, int E, int T, int H, int k, void* out, bool out_bf16,
                           hipStream_t stream);
 
+// combine with dropout of the sum and a residual added (dropout.hip's generator; element
+// (t, h) of out is element t * H + h)
+struct DropoutArgs {
+  const void* residual = nullptr;   // [T, H] or null
+  bool residual_bf16 = false;
+  double p = 0.0;
+  const uint64_t* rng = nullptr;    // device: seed, offset
+};
+hipError_t launch_combine_dropout(const void* y, bool y_bf16, const int* row_pos, const float* weights,
+                                  const int* offsets, int E, int T, int H, int k, const DropoutArgs& drop, void* out,
+                                  bool out_bf16, hipStream_t stream);
+
+struct DropoutLaunch {
+  const void* x;
+  bool x_bf16;
+  const void* residual;   // nullable
+  bool residual_bf16;
+  long long n;
+  double p;
+  const uint64_t* rng;    // device: seed, offset
+  void* out;
+  bool out_bf16;
+};
+hipError_t launch_dropout_add(const DropoutLaunch& p, hipStream_t stream);
+
+// widest row of the layer norm kernels (16 waves of 8 four-element chunks a lane)
+constexpr long long kNormMaxH = 32768;
+struct NormLaunch {
+  const void* x;
+  bool x_bf16;
+  long long T;
+  int H;
+  const void *weight, *bias;   // nullable
+  bool w_bf16;
+  float eps;
+  bool rms;
+  void* y;
+  float *mean, *rstd;          // nullable
+};
+hipError_t launch_norm(const NormLaunch& p, hipStream_t stream);
+struct NormBackwardLaunch {
+  const void *dy, *x;
+  bool x_bf16;
+  long long T;                 // 0: zero parameter gradients
+  int H;
+  const void* weight;          // nullable
+  bool w_bf16;
+  const float *mean, *rstd;    // mean unused with rms
+  bool rms;
+  void* dx;
+  void *dweight, *dbias;       // nullable
+  bool grad_bf16;
+  float* part;                 // norm_backward_workspace_bytes(T, H)
+};
+hipError_t launch_norm_backward(const NormBackwardLaunch& p, hipStream_t stream);
+size_t norm_backward_workspace_bytes(long long T, int H);
+
+// grouped product with 4-bit weights (fourbit.hip)
+struct FourbitLaunch {
+  const void* A;               // bf16 [a_total, K]
+  const int* a_rows;           // nullable: row p of the product reads row a_rows[p] / a_div of A
+  int a_div;
+  long long a_total;
+  const void* codes;           // [E, N, K/2]
+  const void* scales;          // [E, N, K/group] f32 (int4) or e8m0 bytes (mxfp4)
+  bool int4;
+  int group;
+  const int* offsets;
+  int E;
+  long long M_rows, N, K;
+  bool silu;
+  void* C;
+  bool c_f32;                  // else bf16
+};
+hipError_t launch_fourbit(const FourbitLaunch& p, hipStream_t stream);
+// workgroups of a launch (the grid holds at most 2^24 - 1 of 256 threads)
+long long fourbit_workgroups(long long M_rows, int E, long long n_out);
+// n values of whole groups -> codes and scales
+hipError_t launch_quantize_fourbit(const void* w, bool bf16, long long n, bool int4, int group, void* codes,
+                                   void* scales, hipStream_t stream);
+
 }  // namespace moe

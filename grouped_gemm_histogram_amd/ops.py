@@ -20,6 +20,7 @@ from ._lib import MoeAux, load
 
 _DT = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16,
        torch.float8_e4m3fn: _lib.MOE_FP8_E4M3}
+_EL = (torch.float32, torch.bfloat16)
 _EPI = {"none": _lib.MOE_EPI_NONE, "silu_mul": _lib.MOE_EPI_SILU_MUL}
 
 
@@ -35,6 +36,17 @@ def _check(status: int) -> None:
     if status != _lib.MOE_OK:
         lib = load()
         raise RuntimeError(f"{lib.status_string(status).decode()}: {lib.last_error().decode()}")
+
+
+def _run(fn, device: torch.device, *args) -> None:
+    """Calls the library with ``device`` current and its current stream, the last argument, added."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    _check(status)
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None) -> None:
@@ -346,3 +358,263 @@ def backward(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, dout: torch.T
                         _p(dout), _p(g.dx), _p(g.dw13), _p(g.dw2), _DT[grad_dtype], _p(g.dtopk_weights),
                         _p(workspace), workspace.numel(), _stream(x)))
     return g
+
+
+def _fourbit(codes: torch.Tensor, scales: torch.Tensor, device, what: str):
+    """Checks 4-bit codes [E, N, K/2] and their scales; returns (E, N, K, format, group).
+
+    uint8 scales are the e8m0 bytes of mxfp4, float32 scales those of int4.
+    """
+    _need(codes, f"{what}codes", torch.uint8, device=device)
+    _need(scales, f"{what}scales", (torch.uint8, torch.float32), device=device)
+    if codes.dim() != 3 or scales.dim() != 3 or scales.shape[:2] != codes.shape[:2]:
+        raise ValueError(f"{what}codes must be [E, N, K/2] and {what}scales [E, N, K/group]")
+    E, N, half = codes.shape
+    groups = scales.shape[2]
+    if groups == 0 or (2 * half) % groups != 0:
+        raise ValueError(f"{what}scales has {groups} groups for K = {2 * half}")
+    fmt = _lib.MOE_MXFP4 if scales.dtype == torch.uint8 else _lib.MOE_INT4
+    return E, N, 2 * half, fmt, 2 * half // groups
+
+
+def quantize_fourbit(w: torch.Tensor, format: str = "int4", group: Optional[int] = None):
+    """w [E, N, K] (f32 or bf16) -> (codes uint8 [E, N, K/2], scales [E, N, K/group]).
+
+    ``format``: "int4" (codes - 8 times f32 scales; group 32, 64 or 128, default 128) or
+    "mxfp4" (e2m1 codes, e8m0 scale bytes; group 32).  The even channel is in the low nibble.
+    """
+    _need(w, "w", _EL)
+    if w.dim() != 3:
+        raise ValueError(f"w must be [E, N, K], not {tuple(w.shape)}")
+    if format not in ("int4", "mxfp4"):
+        raise ValueError(f"format must be 'int4' or 'mxfp4', not {format!r}")
+    fp = format == "mxfp4"
+    group = group or (32 if fp else 128)
+    E, N, K = w.shape
+    if K % 2 or K % group:
+        raise ValueError(f"K = {K} is not a multiple of group = {group}")
+    codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(E, N, K // group, dtype=torch.uint8 if fp else torch.float32, device=w.device)
+    _run(load().quantize_fourbit, w.device, _p(w), _DT[w.dtype], E, N, K,
+         _lib.MOE_MXFP4 if fp else _lib.MOE_INT4, group, _p(codes), _p(scales))
+    return codes, scales
+
+
+def grouped_matvec_fourbit(a: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                           epilogue: str = "none", gather_rows: Optional[torch.Tensor] = None,
+                           gather_div: int = 1, out_dtype: Optional[torch.dtype] = None,
+                           out: Optional[torch.Tensor] = None):
+    """grouped_gemm on 4-bit weights for few rows per expert: a bf16 [A_rows, K] x codes
+    [E, N, K/2] over segments of offsets -> c [M, N or N/2] (bf16 or f32).
+
+    With ``gather_rows`` product row p reads a[gather_rows[p] // gather_div], as in
+    grouped_gemm_gather.  uint8 scales are mxfp4's, float32 scales int4's.
+    """
+    _need(a, "a", torch.bfloat16)
+    dev = a.device
+    A_rows, K = a.shape
+    E, N, K2, fmt, group = _fourbit(codes, scales, dev, "")
+    if K2 != K:
+        raise ValueError(f"K mismatch: a has {K}, codes have {K2}")
+    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    M = A_rows
+    if gather_rows is not None:
+        _need(gather_rows, "gather_rows", torch.int32, device=dev)
+        M = gather_rows.numel()
+    n_out = N // 2 if epilogue == "silu_mul" else N
+    if out is None:
+        out = torch.empty(M, n_out, dtype=out_dtype or torch.bfloat16, device=dev)
+    _need(out, "out", out_dtype or _EL, (M, n_out), dev)
+    _run(load().grouped_matvec_fourbit, dev, _p(a), A_rows, _p(gather_rows), int(gather_div), _p(codes), _p(scales),
+         fmt, group, _p(offsets), E, M, N, K, _EPI[epilogue], _p(out), _DT[out.dtype])
+    return out
+
+
+def forward_fourbit_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
+    return load().forward_fourbit_workspace(T, H, I, E, k)
+
+
+def forward_fourbit(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor,
+                    w2: torch.Tensor, w2_scale: torch.Tensor, k: int, num_valid_rows: int = -1,
+                    renormalize: bool = True, out_dtype: Optional[torch.dtype] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    return_aux: bool = False):
+    """The whole layer on 4-bit weights, for decode sizes: x bf16 [T, H], logits f32 [T, E],
+    codes w13 [E, 2I, H/2] and w2 [E, H, I/2] with their scales (quantize_fourbit's formats)
+    -> out [T, H] (bf16 or f32)."""
+    _need(x, "x", torch.bfloat16)
+    T, H = x.shape
+    dev = x.device
+    E, I2, H2, fmt, group = _fourbit(w13, w13_scale, dev, "w13 ")
+    E2, Hn, I, fmt2, group2 = _fourbit(w2, w2_scale, dev, "w2 ")
+    if (E2, Hn, 2 * I, H2) != (E, H, I2, H):
+        raise ValueError(f"w13 [{E}, {I2}, {H2}] and w2 [{E2}, {Hn}, {I}] do not fit x [{T}, {H}]")
+    if (fmt, group) != (fmt2, group2):
+        raise ValueError("w13 and w2 must have one format and group")
+    _need(logits, "logits", torch.float32, (T, E), dev)
+    if out is None:
+        out = torch.empty(T, H, dtype=out_dtype or torch.bfloat16, device=dev)
+    _need(out, "out", out_dtype or _EL, (T, H), dev)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(max(lib.forward_fourbit_workspace(T, H, I, E, k), 1), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, device=dev)
+    aux_t = aux_c = None
+    if return_aux:
+        i32 = lambda *shape: torch.empty(*shape, dtype=torch.int32, device=dev)
+        aux_t = ForwardAux(i32(T, k), torch.empty(T, k, dtype=torch.float32, device=dev), i32(E + 1), i32(T * k),
+                           i32(T * k))
+        aux_c = MoeAux(aux_t.topk_ids.data_ptr(), aux_t.topk_weights.data_ptr(), aux_t.offsets.data_ptr(),
+                       aux_t.sorted_rows.data_ptr(), aux_t.row_pos.data_ptr())
+    _run(lib.forward_fourbit, dev, _p(x), _p(logits), _p(w13), _p(w13_scale), _p(w2), _p(w2_scale), fmt, group, T, H,
+         I, E, k, num_valid_rows, int(bool(renormalize)), _p(out), _DT[out.dtype],
+         ctypes.byref(aux_c) if aux_c is not None else None, _p(workspace), workspace.numel())
+    return (out, aux_t) if return_aux else out
+
+
+@dataclass
+class NormStats:
+    mean: Optional[torch.Tensor]  # f32 [T]; None in the root-mean-square form
+    rstd: torch.Tensor            # f32 [T]
+
+
+@dataclass
+class NormGradients:
+    dx: torch.Tensor                   # [T, H]
+    dweight: Optional[torch.Tensor]    # [H]; None without a weight
+    dbias: Optional[torch.Tensor]      # [H]; None unless asked for
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, rms: bool = False, return_stats: bool = False,
+               out: Optional[torch.Tensor] = None):
+    """Layer norm of token rows x [T, H] (f32 or bf16, any H up to 32768) -> y of x's shape and dtype.
+
+    ``rms``: the root-mean-square form (no mean is subtracted).  weight and bias [H], f32 or
+    bf16 (one dtype), may be None.  ``return_stats`` also returns what layer_norm_backward needs.
+    """
+    _need(x, "x", _EL)
+    T, H = x.shape
+    dev = x.device
+    if weight is not None:
+        _need(weight, "weight", _EL, (H,), dev)
+    if bias is not None:
+        _need(bias, "bias", _EL if weight is None else weight.dtype, (H,), dev)
+    params = weight if weight is not None else bias
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out, "out", x.dtype, (T, H), dev)
+    stats = None
+    if return_stats:
+        stats = NormStats(None if rms else torch.empty(T, dtype=torch.float32, device=dev),
+                          torch.empty(T, dtype=torch.float32, device=dev))
+    _run(load().layer_norm, dev, _p(x), _DT[x.dtype], T, H, _p(weight), _p(bias),
+         _lib.MOE_F32 if params is None else _DT[params.dtype], eps, int(bool(rms)), _p(out),
+         _p(stats.mean) if stats else None, _p(stats.rstd) if stats else None)
+    return (out, stats) if return_stats else out
+
+
+def layer_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return load().layer_norm_backward_workspace(T, H)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: NormStats, weight: Optional[torch.Tensor] = None,
+                        bias_grad: bool = False, grad_dtype: torch.dtype = torch.float32,
+                        dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> NormGradients:
+    """Gradients of layer_norm: dy, x [T, H] and the statistics of the forward (stats.mean None:
+    the root-mean-square form) -> dx (x's dtype), dweight and dbias (grad_dtype) [H]."""
+    _need(x, "x", _EL)
+    T, H = x.shape
+    dev = x.device
+    _need(dy, "dy", x.dtype, (T, H), dev)
+    _need(stats.rstd, "stats.rstd", torch.float32, (T,), dev)
+    if stats.mean is not None:
+        _need(stats.mean, "stats.mean", torch.float32, (T,), dev)
+    if weight is not None:
+        _need(weight, "weight", _EL, (H,), dev)
+    if grad_dtype not in _EL:
+        raise ValueError(f"grad_dtype must be float32 or bfloat16, not {grad_dtype}")
+    if dx is None:
+        dx = torch.empty_like(x)
+    _need(dx, "dx", x.dtype, (T, H), dev)
+    new = lambda wanted: torch.empty(H, dtype=grad_dtype, device=dev) if wanted else None
+    g = NormGradients(dx, new(weight is not None), new(bias_grad))
+    lib = load()
+    if workspace is None and (g.dweight is not None or g.dbias is not None):
+        workspace = torch.empty(max(lib.layer_norm_backward_workspace(T, H), 1), dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, device=dev)
+    _run(lib.layer_norm_backward, dev, _p(dy), _p(x), _DT[x.dtype], T, H, _p(weight),
+         _lib.MOE_F32 if weight is None else _DT[weight.dtype], _p(stats.mean), _p(stats.rstd),
+         int(stats.mean is None), _p(dx), _p(g.dweight), _p(g.dbias), _DT[grad_dtype], _p(workspace),
+         0 if workspace is None else workspace.numel())
+    return g
+
+
+def dropout_counters(n: int) -> int:
+    """Counters that a dropout call over n elements uses: what to add to rng[1] between calls."""
+    return (n + 7) // 8
+
+
+def _need_rng(rng: torch.Tensor, device) -> None:
+    _need(rng, "rng", (torch.int64, torch.uint64), (2,), device)
+
+
+def dropout_add(x: torch.Tensor, rng: torch.Tensor, p: float, residual: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None):
+    """residual + dropout(x), or dropout(x) alone; x (f32 or bf16) of any shape.
+
+    ``rng``: GPU int64 (or uint64) [2] holding seed and offset; the mask is a function of them, p
+    and the element's index, so dropout_add_backward with the same rng draws it again.  Advance
+    rng[1] by dropout_counters(x.numel()) between calls.  out (default: the residual's dtype, else
+    x's) may be x or residual.
+    """
+    _need(x, "x", _EL)
+    dev = x.device
+    _need_rng(rng, dev)
+    if residual is not None:
+        _need(residual, "residual", _EL, x.shape, dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or (x.dtype if residual is None else residual.dtype), device=dev)
+    _need(out, "out", out_dtype or _EL, x.shape, dev)
+    _run(load().dropout_add, dev, _p(x), _DT[x.dtype], _p(residual),
+         _lib.MOE_F32 if residual is None else _DT[residual.dtype], x.numel(), p, _p(rng), _p(out), _DT[out.dtype])
+    return out
+
+
+def dropout_add_backward(dout: torch.Tensor, rng: torch.Tensor, p: float, dx_dtype: Optional[torch.dtype] = None,
+                         dx: Optional[torch.Tensor] = None):
+    """Gradient of dropout_add (or unpermute_combine_dropout) with respect to what it dropped, for
+    the same rng and p; the residual's gradient is dout itself."""
+    return dropout_add(dout, rng, p, None, dx_dtype, dx)
+
+
+def unpermute_combine_dropout(y: torch.Tensor, row_pos: torch.Tensor, topk_weights: torch.Tensor,
+                              offsets: torch.Tensor, k: int, rng: torch.Tensor, p: float,
+                              residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                              out: Optional[torch.Tensor] = None):
+    """residual + dropout(unpermute_combine(y, ...)) in one pass: y [R, H] -> out [T, H].
+
+    The mask is dropout_add's for an array [T, H].  out (default: the residual's dtype, else
+    y's) must not overlap residual.
+    """
+    _need(y, "y", _EL)
+    R, H = y.shape
+    T = R // k
+    E = offsets.numel() - 1
+    dev = y.device
+    _need(row_pos, "row_pos", torch.int32, device=dev)
+    _need(topk_weights, "topk_weights", torch.float32, device=dev)
+    _need(offsets, "offsets", torch.int32, device=dev)
+    if row_pos.numel() < T * k or topk_weights.numel() < T * k:
+        raise ValueError("row_pos and topk_weights need T*k entries")
+    _need_rng(rng, dev)
+    if residual is not None:
+        _need(residual, "residual", _EL, (T, H), dev)
+    if out is None:
+        out = torch.empty(T, H, dtype=out_dtype or (y.dtype if residual is None else residual.dtype), device=dev)
+    _need(out, "out", out_dtype or _EL, (T, H), dev)
+    _run(load().unpermute_combine_dropout, dev, _p(y), _DT[y.dtype], _p(row_pos), _p(topk_weights), _p(offsets), E, T,
+         H, k, _p(residual), _lib.MOE_F32 if residual is None else _DT[residual.dtype], p, _p(rng), _p(out),
+         _DT[out.dtype])
+    return out

@@ -58,7 +58,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 4
+#define MOE_ABI_VERSION 5
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 16
 
@@ -73,6 +73,8 @@ typedef enum {
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype_t;
 
 typedef enum { MOE_EPI_NONE = 0, MOE_EPI_SILU_MUL = 1 } moe_epilogue_t;
+
+typedef enum { MOE_INT4 = 0, MOE_MXFP4 = 1 } moe_fourbit_t;
 
 /*
  * moe_route_topk -- the router's choice of a small subset of experts per
@@ -371,6 +373,171 @@ moe_status_t moe_backward(const void* x, const void* w13, const float* w13_scale
                           void* dx, void* dw13, void* dw2, moe_dtype_t grad_dtype,
                           float* dtopk_weights, void* workspace, size_t workspace_bytes,
                           void* stream);
+
+/*
+ * 4-bit weights.  Codes are bytes [E, N, K/2], the even channel of a pair in the
+ * low nibble; one scale belongs to `group` consecutive channels of a weight row:
+ *
+ *   MOE_INT4   value = (code - 8) * scale, f32 scales [E, N, K/group], group
+ *              32, 64 or 128.
+ *   MOE_MXFP4  value = e2m1(code) * 2^(scale - 127), e8m0 scale bytes
+ *              [E, N, K/32], group 32.  e2m1 codes are sign, two exponent bits,
+ *              one mantissa bit: 0 0.5 1 1.5 2 3 4 6 and their negatives.
+ *
+ * K is a multiple of 32 and of group.
+ */
+
+/*
+ * moe_quantize_fourbit -- 4-bit codes and group scales of packed weights.
+ *
+ *   w       [E, N, K] of w_dtype (MOE_F32 or MOE_BF16), finite values.
+ *   codes   out [E, N, K/2]; scales out as above.
+ *
+ * MOE_INT4: scale = amax/7 of the group (1 where that is zero), code = 8 +
+ * round(w/scale) (ties to even).  MOE_MXFP4: scale = 2^(floor(log2 amax) - 2)
+ * (1 for an all-zero group; clamped to a byte), code = w/scale rounded to the
+ * nearest e2m1 value, ties to the even code, magnitudes past 6 to 6.
+ */
+moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E, int64_t N, int64_t K,
+                                  moe_fourbit_t format, int32_t group, void* codes, void* scales,
+                                  void* stream);
+
+/*
+ * moe_grouped_matvec_fourbit -- moe_grouped_gemm (gather_rows null) or
+ * moe_grouped_gemm_gather for 4-bit weights and few rows per expert:
+ *
+ *   for p in [offsets[e], offsets[e+1]):
+ *       acc[p, n] = sum_k A[row(p), k] * value(codes[e, n, k])
+ *
+ *   A            bf16 [A_rows, K], |A| < 2^120 for MOE_INT4.  row(p) = p
+ *                (A_rows >= M_rows), or with gather_rows (device int32
+ *                [M_rows]) gather_rows[p] / gather_div clamped into A.
+ *   codes, scales  4-bit weights [E, N, K], see above.
+ *   offsets      device int32 [E+1], read on the device.
+ *   epi          as for moe_grouped_gemm (SiLU*up: N even, N_out = N/2).
+ *   C            [M_rows, N_out] of c_dtype (MOE_F32 or MOE_BF16), no
+ *                alignment of its rows needed; rows from offsets[E] on are
+ *                written as exact zeros.
+ *
+ * Any number of rows is computed; the weights are read once per 16 rows of an
+ * expert (64 where the launch has more than 8 rows per expert on average), so
+ * with many rows per expert moe_grouped_gemm on bf16 weights is faster.
+ * Accumulation is f32, C is rounded once.  mxfp4 values are taken as bf16
+ * (exact unless they leave bf16's range); int4 values are not rounded at all.
+ */
+moe_status_t moe_grouped_matvec_fourbit(const void* A, int64_t A_rows, const int32_t* gather_rows,
+                                        int32_t gather_div, const void* codes, const void* scales,
+                                        moe_fourbit_t format, int32_t group, const int32_t* offsets, int32_t E,
+                                        int64_t M_rows, int64_t N, int64_t K, moe_epilogue_t epi, void* C,
+                                        moe_dtype_t c_dtype, void* stream);
+
+/* Bytes of device workspace moe_forward_fourbit needs; 0 for invalid arguments. */
+size_t moe_forward_fourbit_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k);
+
+/*
+ * moe_forward_fourbit -- moe_forward with 4-bit weights, for decode sizes: the
+ * same routing, offsets and combine around two moe_grouped_matvec_fourbit
+ * products.  x bf16 [T, H]; h and the expert outputs are rounded to bf16; out
+ * is MOE_BF16 or MOE_F32; H and I are multiples of 32 and of group.  Everything
+ * else (aux and its stage events, workspace, errors) is as in moe_forward; the
+ * activation-staging stage is empty.
+ */
+moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, const void* w13_codes,
+                                 const void* w13_scales, const void* w2_codes, const void* w2_scales,
+                                 moe_fourbit_t format, int32_t group, int64_t T, int64_t H, int64_t I, int32_t E,
+                                 int32_t k, int64_t num_valid_rows, int32_t renormalize, void* out,
+                                 moe_dtype_t out_dtype, moe_aux_t* aux, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * moe_layer_norm -- layer norm of token rows (in front of the router and the
+ * experts), or its root-mean-square form:
+ *
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1/sqrt(mean((x - mean)^2) + eps)
+ *
+ * with mean = 0 when rms is non-zero.
+ *
+ *   x, y         [T, H] of x_dtype (MOE_F32 or MOE_BF16); H any value in
+ *                [1, 32768] (rows need no alignment of their own).  y may be x.
+ *   weight, bias [H] of w_dtype (MOE_F32 or MOE_BF16), aligned to their
+ *                elements; null: ones, zeros.
+ *   eps          finite, >= 0.
+ *   mean, rstd   out f32 [T], nullable; mean is not written with rms.
+ * Statistics and y are computed in f32; y is rounded once.
+ */
+moe_status_t moe_layer_norm(const void* x, moe_dtype_t x_dtype, int64_t T, int64_t H, const void* weight,
+                            const void* bias, moe_dtype_t w_dtype, float eps, int32_t rms, void* y, float* mean,
+                            float* rstd, void* stream);
+
+/* Bytes of device workspace moe_layer_norm_backward needs (partial sums of the
+ * parameter gradients); 0 for invalid arguments. */
+size_t moe_layer_norm_backward_workspace(int64_t T, int64_t H);
+
+/*
+ * moe_layer_norm_backward -- gradients of moe_layer_norm from its statistics.
+ * With xhat = (x - mean) * rstd and g = dy * weight:
+ *
+ *   dx      = rstd * (g - mean(g) - xhat * mean(g * xhat))   (no mean(g) with rms)
+ *   dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy
+ *
+ *   dy, x, dx    [T, H] of x_dtype; dx may be dy or x.
+ *   weight       as given to moe_layer_norm (null: ones).
+ *   mean, rstd   f32 [T] of moe_layer_norm; mean is not read with rms.
+ *   dweight, dbias  out [H] of grad_dtype (MOE_F32 or MOE_BF16), nullable;
+ *                zeros when T = 0.
+ *   workspace    >= moe_layer_norm_backward_workspace(T, H) bytes, 16-byte
+ *                aligned; not needed (may be null) when dweight and dbias are null.
+ * All sums are f32, in a fixed order.
+ */
+moe_status_t moe_layer_norm_backward(const void* dy, const void* x, moe_dtype_t x_dtype, int64_t T, int64_t H,
+                                     const void* weight, moe_dtype_t w_dtype, const float* mean,
+                                     const float* rstd, int32_t rms, void* dx, void* dweight, void* dbias,
+                                     moe_dtype_t grad_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout.  Element i of an array is kept iff a 32-bit uniform u(seed, offset,
+ * i) >= round(p * 2^32).  u comes from the counter-based generator
+ * Philox4x32-10 (Salmon et al., "Parallel Random Numbers: As Easy as 1, 2, 3",
+ * 2011) with the 64-bit seed as key and 128-bit counters of the words (low and
+ * high word of offset + i/8, half, 0): u's high half is 16-bit piece i % 8 of
+ * the output for half = 0 (words in order, low piece of a word first), its low
+ * half the same piece for half = 1.  The mask is recomputed, never stored.
+ *
+ *   rng          device uint64 [2]: seed, offset; read when the kernel runs, so
+ *                a captured graph draws new masks when the caller changes it.
+ *                A call over n elements uses the counters offset + [0, (n+7)/8):
+ *                advance offset by that much between calls.
+ *   p            in [0, 1]; 1 drops every element.  Kept values are scaled by
+ *                1/(1-p).  A dropped element counts as exactly zero, also where
+ *                it is infinite or NaN.
+ */
+
+/*
+ * moe_dropout_add -- out[i] = residual[i] + dropout(x)[i], computed in f32 and
+ * rounded once.  Its backward pass is the same call on the gradient of out,
+ * with the same rng and p and no residual (whose gradient is that of out).
+ *
+ *   x, residual, out  n elements of x_dtype, residual_dtype, out_dtype
+ *                (MOE_F32 or MOE_BF16 each), 16-byte aligned; residual
+ *                nullable.  out may be x or residual if their types agree.
+ */
+moe_status_t moe_dropout_add(const void* x, moe_dtype_t x_dtype, const void* residual,
+                             moe_dtype_t residual_dtype, int64_t n, double p, const uint64_t* rng, void* out,
+                             moe_dtype_t out_dtype, void* stream);
+
+/*
+ * moe_unpermute_combine_dropout -- moe_unpermute_combine with dropout of the
+ * f32 sum (element t*H + h of the layer's output) and a residual added before
+ * the one rounding: the way back into the residual stream in one pass.
+ *
+ *   residual     [T, H] of residual_dtype (MOE_F32 or MOE_BF16), 16-byte
+ *                aligned, nullable; out must not overlap it.
+ */
+moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, const int32_t* row_pos,
+                                           const float* topk_weights, const int32_t* offsets, int32_t E,
+                                           int64_t T, int64_t H, int32_t k, const void* residual,
+                                           moe_dtype_t residual_dtype, double p, const uint64_t* rng, void* out,
+                                           moe_dtype_t out_dtype, void* stream);
 
 /* Short name of a status code. */
 const char* moe_status_string(moe_status_t status);

@@ -23,6 +23,10 @@ fixes another precision):
                  routing held fixed: dx, dW13, dW2 and the routing-weight
                  gradients, by the chain rule through the same per-expert loop.
 
+Around the layer: ``norm.py`` (layer norm and its root-mean-square form, forward and
+backward), ``dropout.py`` (the counter-based generator and dropout with a residual) and
+``fourbit.py`` (what 4-bit codes and group scales stand for, and the coding of weights).
+
 Sources: the transformers PR #45621 write-up ("MoE 및 FP8 커널 최적화"),
 section 2 (sentinel tokens are excluded from the histogram / sorted as the
 largest key; ``offsets[-1]`` is the valid-row count) and section 3 (sentinel
@@ -40,4 +44,4 @@ textbook SwiGLU via torch, torch's e4m3 cast, the valid-row counts the
 transformers write-up prints, invariants).  Nothing here is "parity unpinned".
 """
 
-from . import e4m3, routing, layer, gemm, brute  # noqa: F401
+from . import e4m3, routing, layer, gemm, brute, norm, dropout, fourbit  # noqa: F401
