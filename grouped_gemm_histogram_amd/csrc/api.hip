@@ -818,6 +818,7 @@ moe_status_t moe_grouped_matvec_fourbit(const void* A, int64_t A_rows, const int
   if (moe_status_t s = check_fourbit(format, group, K)) return s;
   const bool silu = epi == MOE_EPI_SILU_MUL;
   MOE_REQUIRE(!silu || N % 2 == 0, "SiLU*up needs an even N");
+  MOE_REQUIRE(N * K / 2 <= kMaxRows, "one expert's codes must span under 2 GiB");
   if (gather_rows)
     MOE_REQUIRE(gather_div >= 1 && gather_div <= MOE_MAX_TOPK, "gather_div=%d outside [1, %d]", gather_div,
                 MOE_MAX_TOPK);
@@ -828,7 +829,7 @@ moe_status_t moe_grouped_matvec_fourbit(const void* A, int64_t A_rows, const int
   MOE_REQUIRE(A && codes && scales && offsets && C, "null pointer argument");
   MOE_REQUIRE(aligned16(A) && aligned16(codes) && aligned16(scales) && aligned16(C),
               "A, codes, scales and C must be 16-byte aligned");
-  if (moe::fourbit_workgroups(M_rows, E, silu ? N / 2 : N) > kMaxWorkgroups)
+  if (moe::fourbit_workgroups(M_rows, E, silu ? N / 2 : N, silu) > kMaxWorkgroups)
     return fail(MOE_ERR_UNSUPPORTED, "%lld rows of %lld columns exceed one launch", (long long)M_rows, (long long)N);
   moe::FourbitLaunch p{};
   p.A = A;
@@ -865,6 +866,7 @@ moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, cons
   MOE_REQUIRE(fourbit_sizes_ok(T, H, I, E, k), "bad sizes");
   if (moe_status_t s = check_fourbit(format, group, H)) return s;
   if (moe_status_t s = check_fourbit(format, group, I)) return s;
+  MOE_REQUIRE(I * H <= kMaxRows, "one expert's codes must span under 2 GiB");
   MOE_REQUIRE(f32_or_bf16(out_dtype), "out_dtype must be MOE_F32 or MOE_BF16");
   const long long R = T * k;
   if (T > 0) {
@@ -873,7 +875,7 @@ moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, cons
     MOE_REQUIRE(aligned16(x) && aligned16(w13_codes) && aligned16(w13_scales) && aligned16(w2_codes) &&
                     aligned16(w2_scales) && aligned16(out),
                 "x, weights, scales and out must be 16-byte aligned");
-    if (std::max(moe::fourbit_workgroups(R, E, I), moe::fourbit_workgroups(R, E, H)) > kMaxWorkgroups)
+    if (std::max(moe::fourbit_workgroups(R, E, I, true), moe::fourbit_workgroups(R, E, H, false)) > kMaxWorkgroups)
       return fail(MOE_ERR_UNSUPPORTED, "%lld routed rows exceed one launch", R);
   }
   const FourbitLayout L = fourbit_layout(T, H, I, E, k);

@@ -21,6 +21,7 @@
 // shared by gate and up.  Its terms are at most 17 times the true ones, 2^-24 each.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "moe.h"
@@ -62,19 +63,16 @@ __device__ __forceinline__ uint4 order_int4(uint4 a) {
                     __builtin_amdgcn_perm(a.w, a.y, 0x05040100u), __builtin_amdgcn_perm(a.w, a.y, 0x07060302u));
 }
 
-// eight e2m1 codes -> bf16 code * scale, in channel order
-__device__ __forceinline__ uint4 unpack_mxfp4(uint32_t v, float scale) {
+// eight e2m1 codes -> bf16 code * 2^(e8m0 - 127), in channel order; the conversion takes its scale
+// from an f32's exponent bits
+__device__ __forceinline__ uint4 unpack_mxfp4(uint32_t v, uint32_t e8m0) {
+  const float scale = __uint_as_float(e8m0 << 23);
   uint4 r;
   r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 0));
   r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 1));
   r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 2));
   r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 3));
   return r;
-}
-
-// An e8m0 byte as f32: 2^(b - 127); 0 is 2^-127, 255 is NaN.
-__device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
-  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
 }
 
 // Where row block `block` of a launch lies: rows [lo, hi) of expert e, or with e < 0 rows
@@ -134,42 +132,98 @@ struct FourbitArgs {
   const int* offsets;
   int E, M_rows, N, K;
   void* C;
+  bool c_f32;
 };
 
-// kGroup: channels per scale (mxfp4: 32).  kTiles column tiles of a wave: gate and up, or one.
-template <bool kInt4, int kGroup, bool kSilu, int MT, bool kF32Out, int kWaves>
-__global__ __launch_bounds__(kWaves * 64) void fourbit_kernel(FourbitArgs p) {
-  constexpr int kTiles = kSilu ? 2 : 1;
+#ifndef FB_WAVES
+#define FB_WAVES 4
+#define FB_NT 4
+#define FB_WG 512
+#endif
+constexpr int kFbWaves = FB_WAVES;
+constexpr int kStep = 256;   // channels of a step: 128 bytes of a weight row, one cache line
+
+// Two registers of a wave, each 8 weight rows x 128 bytes (lane 16 q + c: row c % 8, 16-byte piece
+// q + 4 (c / 8)), into the first and second 64 bytes of all 16 rows (lane 16 q + c: row c, piece q)
+__device__ __forceinline__ void halves(uint32_t& a, uint32_t& b) {
+  // lanes 8..15 of each row of 16 take the other register's lanes 0..7, and the other way round
+  const uint32_t first = __builtin_amdgcn_update_dpp(a, b, 0x128, 0xf, 0xc, false);    // row_ror:8
+  const uint32_t second = __builtin_amdgcn_update_dpp(b, a, 0x128, 0xf, 0x3, false);
+  a = first;
+  b = second;
+}
+
+// LDS of a weight row's scales: whole steps (the missing channels of the last one have scales that
+// do no harm) and one step of padding, so that the 16 rows of a tile start in different banks.
+template <bool kInt4, int kGroup>
+constexpr int kStepScaleBytes = kStep / kGroup * (kInt4 ? 4 : 1);
+__host__ __device__ constexpr int scale_row_bytes(long long K, int step_bytes) {
+  return (int)((K + kStep - 1) / kStep + 1) * step_bytes;
+}
+
+// Copies the scales of a workgroup's weight rows to LDS: 16 lanes a row, 4 bytes a lane (rows of
+// scales start at any byte, global loads take any address).  row(i) is the weight row of LDS row i.
+template <bool kInt4, int kGroup, int kRows, typename Row>
+__device__ __forceinline__ void stage_scales(const uint8_t* __restrict__ scales, Row row, int K, uint8_t* lds) {
+  const int row_bytes = K / kGroup * (kInt4 ? 4 : 1);
+  const int stride = scale_row_bytes(K, kStepScaleBytes<kInt4, kGroup>);
+  const int used = stride - kStepScaleBytes<kInt4, kGroup>;
+  for (int b = (threadIdx.x & 15) * 4; b < used; b += 64) {
+#pragma unroll 4
+    for (int i = threadIdx.x >> 4; i < kRows; i += kFbWaves * 4) {
+      const uint8_t* src = scales + (size_t)row(i) * row_bytes + b;
+      uint32_t v = kInt4 ? 0u : 0x7f7f7f7fu;   // 0, or 2^0
+      if (b + 4 <= row_bytes)
+        __builtin_memcpy(&v, src, 4);
+      else
+        for (int j = 0; b + j < row_bytes; ++j) v = (v & ~(0xffu << (8 * j))) | (uint32_t)src[j] << (8 * j);
+      *reinterpret_cast<uint32_t*>(lds + i * stride + b) = v;
+    }
+  }
+}
+
+// kGroup: channels per scale (mxfp4: 32).  MT row tiles, NT weight tiles of 16 rows (with SiLU * up
+// the even ones are gate and the odd ones up).
+template <bool kInt4, int kGroup, bool kSilu, int MT, int NT>
+__global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p) {
   constexpr int BM = 16 * MT;
-  __shared__ float red[kWaves][MT][kTiles][16][16];
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  constexpr int kCols = (kSilu ? NT / 2 : NT) * 16;   // output columns
+  constexpr int kScaleBytes = kInt4 ? 4 : 1;
+  constexpr int kScaleWords = kStepScaleBytes<kInt4, kGroup> / 4;   // scales of a row per step
+  // the scales of all tiles' rows, and after the loop the waves' sums [wave][tile][row][16]
+  extern __shared__ __align__(16) uint8_t shared[];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, q = lane >> 4;
   const int n_out = kSilu ? p.N / 2 : p.N;
-  const int tiles = (n_out + 15) / 16;
-  const int n0 = (int)(blockIdx.x % tiles) * 16;
-  const RowBlock blk = find_block(p.offsets, p.E, p.M_rows, BM, blockIdx.x / tiles);
+  const int groups = (n_out + kCols - 1) / kCols;
+  const int n0 = (int)(blockIdx.x % groups) * kCols;
+  const RowBlock blk = find_block(p.offsets, p.E, p.M_rows, BM, blockIdx.x / groups);
   auto store = [&](int r, int n, float v) {
     const size_t at = (size_t)r * n_out + n;
-    if constexpr (kF32Out)
+    if (p.c_f32)
       static_cast<float*>(p.C)[at] = v;
     else
       static_cast<uint16_t*>(p.C)[at] = f32_to_bf16_bits(v);
   };
   if (blk.e < 0) {   // rows without an expert are zero
-    for (int i = threadIdx.x; i < (blk.hi - blk.lo) * 16; i += kWaves * 64)
-      if (n0 + (i & 15) < n_out) store(blk.lo + (i >> 4), n0 + (i & 15), 0.0f);
+    for (int i = threadIdx.x; i < (blk.hi - blk.lo) * kCols; i += kFbWaves * 64)
+      if (n0 + i % kCols < n_out) store(blk.lo + i / kCols, n0 + i % kCols, 0.0f);
     return;
   }
   const int K = p.K;
-  // this lane's column of each tile and its row of each row tile (surplus ones repeat the last)
-  const uint8_t* wp[kTiles];
-  const uint8_t* sp[kTiles];
-  constexpr int kScaleBytes = kInt4 ? 4 : 1;
+  // the expert's codes, under 2 GiB: an offset with the top bit set is past their end and loads zeros
+  const auto codes = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.codes) + (size_t)blk.e * p.N * (K / 2), 0, (uint32_t)p.N * (uint32_t)(K / 2), 0x00020000);
+  // weight row `i` of tile t; rows past the last repeat it
+  auto wrow = [&](int t, int i) {
+    return (uint32_t)((kSilu && (t & 1) ? n_out : 0) + min(n0 + (kSilu ? t / 2 : t) * 16 + i, n_out - 1));
+  };
+  const int piece = q + 4 * (col >> 3);   // this lane's 16 bytes of a step when it loads codes
+  uint32_t wat[NT][2];                    // where it loads codes of rows col % 8 and 8 + col % 8
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const size_t n = (size_t)blk.e * p.N + (size_t)t * n_out + min(n0 + col, n_out - 1);
-    wp[t] = p.codes + n * (K / 2);
-    sp[t] = static_cast<const uint8_t*>(p.scales) + n * (K / kGroup) * kScaleBytes;
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) wat[t][h] = wrow(t, (col & 7) + 8 * h) * (uint32_t)(K / 2) + 16 * piece;
   }
   const uint16_t* ap[MT];
 #pragma unroll
@@ -178,96 +232,117 @@ __global__ __launch_bounds__(kWaves * 64) void fourbit_kernel(FourbitArgs p) {
     if (p.a_rows) r = min(max(p.a_rows[r] / p.a_div, 0), p.A_rows - 1);
     ap[m] = p.A + (size_t)r * K;
   }
-  f32x4 acc[MT][kTiles];
+  f32x4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // a step is 128 channels: 16 bytes of codes a lane and tile
-  for (int k0 = wave * 128; k0 < K; k0 += kWaves * 128) {
-    const bool mine = k0 + 32 * q < K;   // K % 32 == 0: a lane's 32 channels are all in the row or none
-    uint32_t w[kTiles][4];
+  struct Weights {
+    uint4 c[2];
+  };
+  // K % 32 == 0: a lane's 32 channels are all in the row or none
+  auto load_weights = [&](int k, int t, Weights& w) {
+    const uint32_t past = k + 32 * piece < K ? 0u : 0x80000000u;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (mine) v = *reinterpret_cast<const uint4*>(wp[t] + (k0 + 32 * q) / 2);
-      w[t][0] = v.x; w[t][1] = v.y; w[t][2] = v.z; w[t][3] = v.w;
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(codes, (int)(wat[t][h] | past), k / 2, 0);
+      w.c[h] = make_uint4(v[0], v[1], v[2], v[3]);
     }
+  };
+  uint4 a[MT][8];
+  const int scale_stride = scale_row_bytes(K, 4 * kScaleWords);
+  auto multiply = [&](int k, int t, const Weights& w) {
+    uint32_t c[2][4] = {{w.c[0].x, w.c[0].y, w.c[0].z, w.c[0].w}, {w.c[1].x, w.c[1].y, w.c[1].z, w.c[1].w}};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) halves(c[0][j], c[1][j]);
+    transpose4(c[0]);
+    transpose4(c[1]);
+    uint32_t s[kScaleWords];
+    __builtin_memcpy(s, __builtin_assume_aligned(shared + (t * 16 + col) * scale_stride + k / kGroup * kScaleBytes,
+                                                 kScaleWords >= 4 ? 16 : 8),
+                     4 * kScaleWords);
     if constexpr (kInt4) {
+      // opaque to the compiler, so that each tile makes the offset's products anew: kept for all
+      // tiles they would take 4 registers per 32 channels
+      uint32_t c136 = 0xc308c308u;
+      asm volatile("" : "+v"(c136));
+      const bf16x8 b136 = as_bf16x8(make_uint4(c136, c136, c136, c136));
+      f32x4 d[MT];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) transpose4(w[t]);
-      f32x4 d[MT][kTiles];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k0 + 32 * j >= K) break;
-        if (32 * j % kGroup == 0)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) d[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < 8; ++j) {
+        const bf16x8 b = as_bf16x8(unpack_int4(c[j >> 2][j & 3]));
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const bf16x8 a = as_bf16x8(order_int4(*reinterpret_cast<const uint4*>(ap[m] + k0 + 32 * j + 8 * q)));
-          const uint32_t c136 = 0xc308c308u;
-          const f32x4 off = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              a, as_bf16x8(make_uint4(c136, c136, c136, c136)), f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+          if (32 * j % kGroup == 0) d[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m][j]), b136, d[m], 0, 0, 0);
+          d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m][j]), b, d[m], 0, 0, 0);
+          if (32 * (j + 1) % kGroup == 0)
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-            d[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf16x8(unpack_int4(w[t][j])), d[m][t] + off, 0, 0, 0);
-        }
-        if (32 * (j + 1) % kGroup == 0 || k0 + 32 * (j + 1) >= K) {
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            const float s = reinterpret_cast<const float*>(sp[t])[(k0 + 32 * j) / kGroup];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(s, d[m][t][i], acc[m][t][i]);
-          }
+            for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(__uint_as_float(s[32 * j / kGroup]), d[m][i], acc[m][t][i]);
         }
       }
     } else {
-      float s[kTiles];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) s[t] = mine ? e8m0_to_f32(sp[t][k0 / 32 + q]) : 1.0f;
+      for (int j = 0; j < 8; ++j) {
+        const bf16x8 b = as_bf16x8(unpack_mxfp4(c[j >> 2][j & 3], s[j >> 2] >> (8 * (j & 3)) & 0xff));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8 b[kTiles];
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) b[t] = as_bf16x8(unpack_mxfp4(w[t][j], s[t]));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (mine) v = *reinterpret_cast<const uint4*>(ap[m] + k0 + 32 * q + 8 * j);
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(v), b[t], acc[m][t], 0, 0, 0);
-        }
+        for (int m = 0; m < MT; ++m)
+          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m][j]), b, acc[m][t], 0, 0, 0);
       }
     }
+  };
+  // every tile's weights of a step are in flight at once; a tile's next ones are asked for as
+  // soon as it has been multiplied
+  Weights w[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) load_weights(wave * kStep, t, w[t]);
+  stage_scales<kInt4, kGroup, NT * 16>(
+      static_cast<const uint8_t*>(p.scales) + (size_t)blk.e * p.N * (K / kGroup) * kScaleBytes,
+      [&](int i) { return wrow(i >> 4, i & 15); }, K, shared);
+  __syncthreads();
+  for (int k = wave * kStep; k < K; k += kFbWaves * kStep) {
+    // MFMA j has channels 32 j + 8 q onwards of the step; channels past K are zero
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a[m][j] = make_uint4(0, 0, 0, 0);
+        if (k + 32 * j < K) a[m][j] = *reinterpret_cast<const uint4*>(ap[m] + k + 32 * j + 8 * q);
+        if constexpr (kInt4) a[m][j] = order_int4(a[m][j]);
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      multiply(k, t, w[t]);
+      load_weights(k + kFbWaves * kStep, t, w[t]);   // past K: zeros, without a read
+      __builtin_amdgcn_sched_barrier(0);   // a tile's temporaries end before the next tile's begin
+    }
   }
+  __syncthreads();   // the scales have been read
+  const int rows = blk.hi - blk.lo;
+  float* red = reinterpret_cast<float*>(shared);
+  auto at = [&](int v, int t, int r, int c) { return ((v * NT + t) * BM + r) * 16 + c; };
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[wave][m][t][4 * q + i][col] = acc[m][t][i];
+      for (int i = 0; i < 4; ++i)
+        if (m * 16 + 4 * q + i < rows) red[at(wave, t, m * 16 + 4 * q + i, col)] = acc[m][t][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < BM * 16; i += kWaves * 64) {
-    const int r = i >> 4, c = i & 15;
-    float s[kTiles];
+  for (int i = threadIdx.x; i < rows * kCols; i += kFbWaves * 64) {
+    const int r = i / kCols, c = i % kCols;
+    if (n0 + c >= n_out) continue;
+    auto sum = [&](int t) {
+      float s = red[at(0, t, r, c & 15)];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      s[t] = red[0][r >> 4][t][r & 15][c];
-#pragma unroll
-      for (int v = 1; v < kWaves; ++v) s[t] += red[v][r >> 4][t][r & 15][c];
-    }
-    if (blk.lo + r < blk.hi && n0 + c < n_out) {
-      float out = s[0];
-      if constexpr (kSilu) out = silu_mul(s[0], s[kTiles - 1]);
-      store(blk.lo + r, n0 + c, out);
-    }
+      for (int v = 1; v < kFbWaves; ++v) s += red[at(v, t, r, c & 15)];
+      return s;
+    };
+    if constexpr (kSilu)
+      store(blk.lo + r, n0 + c, silu_mul(sum(c / 16 * 2), sum(c / 16 * 2 + 1)));
+    else
+      store(blk.lo + r, n0 + c, sum(c / 16));
   }
 }
 
@@ -276,34 +351,65 @@ static long long fourbit_blocks(long long M_rows, int E, int BM) {
   return std::min<long long>(M_rows, M_rows / BM + std::min<long long>(E, M_rows) + 1);
 }
 
-// row tiles of 16 per row block
-static int fourbit_row_tiles(long long M_rows, int E) { return M_rows <= 8ll * E ? 1 : 4; }
+// How a launch is cut: row tiles per row block by the rows an expert has on average, weight tiles
+// per workgroup by how many workgroups that leaves.
+constexpr int kMaxNT = FB_NT, kMinWg = FB_WG;
 
-long long fourbit_workgroups(long long M_rows, int E, long long n_out) {
-  return (n_out + 15) / 16 * fourbit_blocks(M_rows, E, 16 * fourbit_row_tiles(M_rows, E));
+struct FourbitCut {
+  int MT, NT;
+  long long workgroups;
+};
+
+static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, bool silu) {
+  FourbitCut c;
+  c.MT = M_rows <= 8ll * E ? 1 : M_rows <= 24ll * E ? 2 : 4;
+  const long long blocks = fourbit_blocks(M_rows, E, 16 * c.MT);
+  const auto wgs = [&](int nt) { return blocks * ((n_out + 16 * nt - 1) / (16 * nt)); };
+  int nt = c.MT == 4 ? 1 : silu || c.MT == 2 ? kMaxNT / 2 : kMaxNT;   // output tiles
+  if (c.MT == 2 && silu) nt = kMaxNT / 4;
+  if (c.MT == 1)
+    while (nt > 1 && wgs(nt) < kMinWg) nt /= 2;
+  c.NT = silu ? 2 * nt : nt;
+  c.workgroups = wgs(nt);
+  return c;
 }
 
-template <bool kInt4, int kGroup, bool kSilu, int MT>
-static hipError_t launch_fourbit_t(const FourbitLaunch& p, hipStream_t stream) {
-  constexpr int kWaves = 4;
-  constexpr int BM = 16 * MT;
-  const int n_out = (int)(kSilu ? p.N / 2 : p.N);
-  const long long blocks = fourbit_blocks(p.M_rows, p.E, BM);
-  FourbitArgs a{static_cast<const uint16_t*>(p.A), p.a_rows, p.a_div, (int)p.a_total,
-                static_cast<const uint8_t*>(p.codes), p.scales, p.offsets, p.E, (int)p.M_rows, (int)p.N, (int)p.K, p.C};
-  const dim3 grid((unsigned)((n_out + 15) / 16 * blocks)), block(kWaves * 64);
-  if (p.c_f32)
-    hipLaunchKernelGGL((fourbit_kernel<kInt4, kGroup, kSilu, MT, true, kWaves>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((fourbit_kernel<kInt4, kGroup, kSilu, MT, false, kWaves>), grid, block, 0, stream, a);
-  return hipGetLastError();
+// the scales of the tiles' rows; afterwards the waves' sums
+static int fourbit_lds(int MT, int NT, long long K, int step_bytes) {
+  return std::max(NT * 16 * scale_row_bytes(K, step_bytes), kFbWaves * NT * MT * 1024);
+}
+
+long long fourbit_workgroups(long long M_rows, int E, long long n_out, bool silu) {
+  return fourbit_cut(M_rows, E, n_out, silu).workgroups;
+}
+
+template <bool kInt4, int kGroup, bool kSilu>
+static hipError_t launch_fourbit_s(const FourbitLaunch& p, hipStream_t stream) {
+  const FourbitCut cut = fourbit_cut(p.M_rows, p.E, kSilu ? p.N / 2 : p.N, kSilu);
+  const FourbitArgs a{static_cast<const uint16_t*>(p.A), p.a_rows, p.a_div, (int)p.a_total,
+                      static_cast<const uint8_t*>(p.codes), p.scales, p.offsets, p.E, (int)p.M_rows, (int)p.N,
+                      (int)p.K, p.C, p.c_f32};
+  const dim3 grid((unsigned)cut.workgroups), block(kFbWaves * 64);
+  const int lds = fourbit_lds(cut.MT, cut.NT, p.K, kStepScaleBytes<kInt4, kGroup>);
+  constexpr int kPer = kSilu ? 2 : 1;   // weight tiles per output tile
+#define MOE_FOURBIT(MT_, NT_)                                                                             \
+  if (cut.MT == MT_ && cut.NT == NT_ * kPer) {                                                            \
+    hipLaunchKernelGGL((fourbit_kernel<kInt4, kGroup, kSilu, MT_, NT_ * kPer>), grid, block, lds, stream, a); \
+    return hipGetLastError();                                                                               \
+  }
+  MOE_FOURBIT(1, 1)
+  if constexpr (kMaxNT >= 4 || !kSilu) { MOE_FOURBIT(1, 2) }
+  if constexpr (kMaxNT / kPer >= 4) { MOE_FOURBIT(1, 4) }
+  if constexpr (kMaxNT / kPer >= 8) { MOE_FOURBIT(1, 8) }
+  MOE_FOURBIT(2, (kMaxNT / 2 / kPer))
+  MOE_FOURBIT(4, 1)
+#undef MOE_FOURBIT
+  return hipErrorInvalidValue;
 }
 
 template <bool kInt4, int kGroup>
 static hipError_t launch_fourbit_g(const FourbitLaunch& p, hipStream_t stream) {
-  const bool one = fourbit_row_tiles(p.M_rows, p.E) == 1;
-  if (p.silu) return one ? launch_fourbit_t<kInt4, kGroup, true, 1>(p, stream) : launch_fourbit_t<kInt4, kGroup, true, 4>(p, stream);
-  return one ? launch_fourbit_t<kInt4, kGroup, false, 1>(p, stream) : launch_fourbit_t<kInt4, kGroup, false, 4>(p, stream);
+  return p.silu ? launch_fourbit_s<kInt4, kGroup, true>(p, stream) : launch_fourbit_s<kInt4, kGroup, false>(p, stream);
 }
 
 hipError_t launch_fourbit(const FourbitLaunch& p, hipStream_t stream) {
