@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "direct_load.h"
 #include "launch.h"
 #include "moe.h"
 #include "rows_device.h"
@@ -75,52 +76,57 @@ __device__ __forceinline__ uint4 unpack_mxfp4(uint32_t v, uint32_t e8m0) {
   return r;
 }
 
-// Where row block `block` of a launch lies: rows [lo, hi) of expert e, or with e < 0 rows
-// [lo, hi) past the last valid row.  Every lane gets the result; all 64 lanes take part.
+// The row blocks of a launch: every expert's rows in blocks of BM, expert by expert.  Each lane keeps
+// the running count of its consecutive experts' blocks; all 64 lanes take part in each call.
 struct RowBlock {
-  int e, lo, hi;
+  int e, lo, hi;   // rows [lo, hi) of expert e
 };
 
-__device__ __forceinline__ RowBlock find_block(const int* __restrict__ offsets, int E, int M_rows, int BM, int block) {
-  const int lane = lane_id();
-  const int per = (E + kWave - 1) / kWave;   // consecutive experts per lane
-  auto at = [&](int e) { return min(max(offsets[min(e, E)], 0), M_rows); };
-  int mine = 0;
-  for (int i = 0, lo = at(lane * per); i < per; ++i) {
-    const int hi = at(lane * per + i + 1);
-    mine += max(hi - lo + BM - 1, 0) / BM;
-    lo = hi;
-  }
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int up = __shfl_up(incl, o, kWave);
-    if (lane >= o) incl += up;
-  }
-  const uint64_t below = __ballot(incl > block);
-  if (below == 0) {   // past the experts' blocks: rows without an expert
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    const int V = at(E);
-    const long long lo = V + (long long)(block - total) * BM;
-    RowBlock r{-1, M_rows, M_rows};
-    if (lo < M_rows) r = {-1, (int)lo, min((int)lo + BM, M_rows)};
-    return r;
-  }
-  const int owner = __builtin_ctzll(below);
-  int rest = block - (__shfl(incl, owner, kWave) - __shfl(mine, owner, kWave));
-  RowBlock r{-1, M_rows, M_rows};
-  for (int i = 0, lo = at(owner * per); i < per; ++i) {
-    const int hi = at(owner * per + i + 1);
-    const int nb = max(hi - lo + BM - 1, 0) / BM;
-    if (rest < nb) {
-      r = {owner * per + i, lo + rest * BM, min(lo + (rest + 1) * BM, hi)};
-      break;
+// a value that is the same in all lanes, into a scalar register (quotients are computed in vector ones)
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+struct RowBlocks {
+  const int* offsets;
+  int E, M_rows, BM, per;
+  int lo0, hi0, mine, incl;
+
+  __device__ __forceinline__ int at(int e) const { return min(max(offsets[min(e, E)], 0), M_rows); }
+  __device__ __forceinline__ int blocks(int lo, int hi) const { return max(hi - lo + BM - 1, 0) / BM; }
+
+  __device__ __forceinline__ RowBlocks(const int* offsets_, int E_, int M_rows_, int BM_)
+      : offsets(offsets_), E(E_), M_rows(M_rows_), BM(BM_), per((E_ + kWave - 1) / kWave) {
+    const int lane = lane_id();
+    lo0 = at(lane * per);
+    mine = 0;
+    for (int i = 0, lo = lo0; i < per; ++i) {
+      const int hi = at(lane * per + i + 1);
+      mine += blocks(lo, hi);
+      lo = hi;
+      if (i == 0) hi0 = hi;
     }
-    rest -= nb;
-    lo = hi;
+    incl = mine;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int up = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += up;
+    }
   }
-  return r;
-}
+
+  __device__ __forceinline__ int count() const { return __builtin_amdgcn_readlane(incl, 63); }
+
+  __device__ __forceinline__ RowBlock find(int block) const {   // 0 <= block < count()
+    const int owner = __builtin_ctzll(__ballot(incl > block) | (1ull << 63));
+    int rest = block - (__builtin_amdgcn_readlane(incl, owner) - __builtin_amdgcn_readlane(mine, owner));
+    int lo = __builtin_amdgcn_readlane(lo0, owner), hi = __builtin_amdgcn_readlane(hi0, owner);
+    int i = 0;
+    for (; i + 1 < per && rest >= blocks(lo, hi); ++i) {
+      rest -= blocks(lo, hi);
+      lo = hi;
+      hi = uniform(at(owner * per + i + 2));
+    }
+    return {uniform(owner * per + i), uniform(lo + rest * BM), uniform(min(lo + (rest + 1) * BM, hi))};
+  }
+};
 
 struct FourbitArgs {
   const uint16_t* A;
@@ -196,8 +202,16 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
   const int col = lane & 15, q = lane >> 4;
   const int n_out = kSilu ? p.N / 2 : p.N;
   const int groups = (n_out + kCols - 1) / kCols;
-  const int n0 = (int)(blockIdx.x % groups) * kCols;
-  const RowBlock blk = find_block(p.offsets, p.E, p.M_rows, BM, blockIdx.x / groups);
+  const int block = uniform(blockIdx.x / groups), n0 = ((int)blockIdx.x - block * groups) * kCols;
+  const RowBlocks rows_of(p.offsets, p.E, p.M_rows, BM);
+  const int past = block - rows_of.count();
+  RowBlock blk;
+  if (past < 0) {
+    blk = rows_of.find(block);
+  } else {   // rows without an expert
+    const int lo = (int)min((long long)rows_of.at(p.E) + (long long)past * BM, (long long)p.M_rows);
+    blk = {-1, lo, (int)min((long long)lo + BM, (long long)p.M_rows)};
+  }
   auto store = [&](int r, int n, float v) {
     const size_t at = (size_t)r * n_out + n;
     if (p.c_f32)
@@ -351,6 +365,329 @@ static long long fourbit_blocks(long long M_rows, int E, int BM) {
   return std::min<long long>(M_rows, M_rows / BM + std::min<long long>(E, M_rows) + 1);
 }
 
+// ---------------------------------------------------------------- few rows per expert: streaming
+//
+// A launch is a fixed number of workgroups of eight waves.  Each takes an even share of the items
+// (a block of up to 16 rows of one expert, 16 weight rows; with SiLU * up 8 gate and 8 up rows) in
+// order, so that it reads consecutive weight rows, and streams them through a ring of LDS slots by
+// direct loads of 1 KiB: all slots but one are in flight while one is multiplied, without a register
+// for it.  Wave w has the activations of S steps of 128 channels in registers for as long as the
+// row block lasts; the waves' f32 sums meet in LDS in wave order.  One barrier an item: behind it
+// the next item's bytes have landed, the previous item's slot is free and its sums are complete.
+//
+// A weight row's 16-byte pieces lie in its LDS row in the order piece ^ swizzle, chosen so that the
+// 16 lanes that read one piece of 16 rows hit different banks.
+
+constexpr int kStreamWaves = 8;
+constexpr int kStreamMaxS = 7;
+
+// 16-byte pieces of a row of `pieces` are stored at piece ^ row_swizzle(pieces, row), row < 16: with
+// G the largest power of two (to 16) in `pieces`, rows row + 16 / G start in the same bank, and
+// differ by the swizzle within a group of G pieces
+__device__ __forceinline__ int row_swizzle(int pieces, int row) {
+  const int a = min(__builtin_ctz(pieces), 4);
+  return row >> (4 - a) & ((1 << a) - 1);
+}
+
+template <bool kInt4, int kGroup, int S>
+struct StreamCfg {
+  static constexpr int W = kStreamWaves;
+  static constexpr int kScaleBytes = kInt4 ? 4 : 1;
+  static constexpr int kMaxK = W * S * 128;
+  // KiB of LDS: one segment (8 rows) of codes and of scales
+  static constexpr int kCodeKb = (8 * kMaxK / 2 + 1023) / 1024;
+  static constexpr int kScaleKb = (8 * (kMaxK / kGroup) * kScaleBytes + (kInt4 ? 0 : 15) + 1023) / 1024;
+  // runtime: the scales are copied from the aligned 16 bytes that hold their first one, so rows of
+  // no whole 16 bytes take up to 15 more (int4's shorter rows are 4 bytes less each: still within kScaleKb)
+  __device__ static int scale_kb(int row_bytes) { return (8 * row_bytes + (row_bytes % 16 ? 15 : 0) + 1023) / 1024; }
+  static constexpr int kSlotKb = 2 * (kCodeKb + kScaleKb);
+  static constexpr int kScaleLoads = (2 * kScaleKb + W - 1) / W;   // a wave's per item
+  static constexpr int kLoads = S + kScaleLoads;
+  static constexpr int kFixedKb = 2 * W + 1;   // two sets of sums, and a place for surplus loads
+  // two workgroups per CU where two slots each fit, else one
+  static constexpr int kPerCu = 2 * (2 * kSlotKb + kFixedKb) <= 160 ? 2 : 1;
+  static constexpr int kRingKb = 160 / kPerCu - kFixedKb;
+  static constexpr int kMaxSlots = std::min(8, 63 / kLoads + 2);   // vmcnt counts to 63
+  static_assert(kRingKb >= 2 * kSlotKb, "ring");
+};
+
+template <bool kInt4, int kGroup, bool kSilu, int S>
+__global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kPerCu * 2)) void fourbit_stream_kernel(
+    FourbitArgs p) {
+  using Cfg = StreamCfg<kInt4, kGroup, S>;
+  constexpr int W = kStreamWaves;
+  constexpr int kRows = kSilu ? 8 : 16;   // output columns of an item
+  constexpr int kWords = kInt4 ? S * (128 / kGroup) : S;   // words of scales a lane needs per item
+  constexpr int kReads = kInt4 ? kWords : kWords + 1;      // mxfp4's start at any byte
+  __shared__ __align__(16) uint8_t ring[Cfg::kRingKb * 1024];
+  __shared__ __align__(16) uint8_t spare[1024];
+  __shared__ float red[2][W][16][16];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, q = lane >> 4;
+  const int K = p.K;
+  const int n_out = kSilu ? p.N / 2 : p.N;
+  const int tiles = (n_out + kRows - 1) / kRows;
+  auto store = [&](int r, int n, float v) {
+    const size_t at = (size_t)r * n_out + n;
+    if (p.c_f32)
+      static_cast<float*>(p.C)[at] = v;
+    else
+      static_cast<uint16_t*>(p.C)[at] = f32_to_bf16_bits(v);
+  };
+  const RowBlocks rows_of(p.offsets, p.E, p.M_rows, 16);
+  // rows without an expert are zero
+  {
+    const int V = rows_of.at(p.E);
+    const long long n = (long long)(p.M_rows - V) * n_out;
+    for (long long i = (long long)blockIdx.x * W * 64 + threadIdx.x; i < n;
+         i += (long long)gridDim.x * W * 64)
+      store(V + (int)(i / n_out), (int)(i % n_out), 0.0f);
+  }
+  const int items = rows_of.count() * tiles;
+  const int share = uniform(items / (int)gridDim.x), extra = items - share * (int)gridDim.x;
+  const int first = (int)blockIdx.x * share + min((int)blockIdx.x, extra);
+  const int n = share + ((int)blockIdx.x < extra ? 1 : 0);
+  if (n == 0) return;
+
+  // ---- this lane's part of the direct loads
+  const int pieces = K / 32, row_bytes = K / 2;
+  const int code_kb = (8 * row_bytes + 1023) / 1024;      // a segment's loads
+  uint32_t code_at[S];                                     // source, from an item's first row
+  int code_to[S];                                          // target, from the slot; < 0: the spare KiB
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    const int load = wave * S + j, seg = (load >= code_kb) + (load >= 2 * code_kb);
+    const int i = min((load - seg * code_kb) * 64 + lane, 8 * pieces - 1);   // piece of the segment, as it lies in LDS
+    int r = 0;
+#pragma unroll
+    for (int m = 1; m < 8; ++m) r += i >= m * pieces;
+    const int pos = i - r * pieces;
+    const int row = kSilu ? min(r, n_out - 1) : min(seg * 8 + r, n_out - 1);
+    code_at[j] = (uint32_t)(row + (kSilu ? seg * n_out : 0)) * (uint32_t)row_bytes +
+                 (uint32_t)(pos ^ row_swizzle(pieces, seg * 8 + r)) * 16u;
+    code_to[j] = seg < 2 ? seg * code_kb * 1024 + (load - seg * code_kb) * 1024 : -1;
+    if (seg >= 2) code_at[j] = 0;
+  }
+  const int scale_row = K / kGroup * Cfg::kScaleBytes;     // bytes of scales of a weight row
+  const int scale_pieces = scale_row % 16 == 0 ? scale_row / 16 : 1;   // odd rows are not swizzled
+  const int rows0 = min(8, n_out);                         // rows of a segment that exist
+  const int second = kSilu ? n_out : n_out > 8 ? 8 : 0;    // first row of the second segment
+  const int rows1 = kSilu ? rows0 : max(min(8, n_out - 8), 1);
+  const int scale_base = 2 * code_kb * 1024;
+  const int scale_kb = Cfg::scale_kb(scale_row);
+  const int slot_bytes = 2 * (code_kb + scale_kb) * 1024;
+  const int slots = uniform(min(Cfg::kRingKb * 1024 / slot_bytes, Cfg::kMaxSlots));
+  int scale_i[Cfg::kScaleLoads];                           // source piece
+#pragma unroll
+  for (int j = 0; j < Cfg::kScaleLoads; ++j) {
+    const int load = wave * Cfg::kScaleLoads + j, seg = (load >= scale_kb) + (load >= 2 * scale_kb);
+    const int i = (load - seg * scale_kb) * 64 + lane;
+    int r = 0;
+#pragma unroll
+    for (int m = 1; m <= 8; ++m) r += i >= m * scale_pieces;
+    scale_i[j] = i ^ (scale_row % 16 == 0 && r < 8 ? row_swizzle(scale_pieces, seg * 8 + r) : 0);
+  }
+
+  using Lds = __attribute__((address_space(3))) uint8_t*;
+  const uint32_t ring_at = (uint32_t)(uintptr_t)(Lds)ring, spare_at = (uint32_t)(uintptr_t)(Lds)spare;
+  // first weight row of a tile; the last tile of several reaches back to have all its rows
+  auto row0_of = [&](int tile) { return max(min(tile * kRows, n_out - kRows), 0); };
+  auto issue = [&](const RowBlock& b, int tile, int slot) {
+    const size_t row = (size_t)b.e * p.N + row0_of(tile);
+    const uint8_t* codes = uniform_ptr(p.codes + row * row_bytes);
+    const uint32_t to = ring_at + slot * slot_bytes;
+#pragma unroll
+    for (int j = 0; j < S; ++j)
+      dma16(uniform_u32(code_to[j] < 0 ? spare_at : to + code_to[j]), codes, code_at[j]);
+#pragma unroll
+    for (int j = 0; j < Cfg::kScaleLoads; ++j) {
+      const int load = wave * Cfg::kScaleLoads + j, seg = (load >= scale_kb) + (load >= 2 * scale_kb);
+      const uint8_t* from = static_cast<const uint8_t*>(p.scales) + (row + (seg == 1 ? second : 0)) * scale_row;
+      const int shift = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+      const int end = (shift + (seg == 1 ? rows1 : rows0) * scale_row - 1) >> 4;   // last piece with a scale in it
+      dma16(uniform_u32(seg < 2 ? to + scale_base + load * 1024 : spare_at), uniform_ptr(from - shift),
+            (uint32_t)(seg < 2 ? min(scale_i[j], end) : 0) * 16u);
+    }
+  };
+
+  // ---- this lane's part of the products
+  const int wr = col & 7, wseg = col >> 3;
+  int code_from[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int piece = min(4 * (wave * S + s) + q, pieces - 1);
+    code_from[s] = wseg * code_kb * 1024 + wr * row_bytes + ((piece ^ row_swizzle(pieces, col)) << 4);
+  }
+  // int4: where a step's scales start (they lie in one 16-byte piece); mxfp4: each word
+  constexpr int kFrom = kInt4 ? S : kReads, kFromWords = kInt4 ? 128 / kGroup : 1;
+  int scale_from[kFrom];
+  const int scale_swz = scale_row % 16 == 0 ? row_swizzle(scale_pieces, col) : 0;
+  const int scale_first = wave * (S * 128 / kGroup) * Cfg::kScaleBytes;   // byte of a row's scales
+#pragma unroll
+  for (int i = 0; i < kFrom; ++i) {
+    const int b = scale_first + 4 * kFromWords * i;
+    scale_from[i] = scale_base + wseg * scale_kb * 1024 + wr * scale_row + (((b >> 4) ^ scale_swz) << 4) + (b & 15);
+  }
+  uint32_t scale_ok[kWords];   // bits of the words that are scales of channels below K
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const int there = scale_row - scale_first - 4 * i;
+    scale_ok[i] = there >= 4 ? ~0u : there <= 0 ? 0u : (1u << (8 * there)) - 1;
+  }
+  bf16x8 a[S][4];
+  // int4: -136 times the sum of each group's activations, kept with the activations; groups of 32
+  // would take as many registers as those, so their offsets are made again for each item
+  constexpr bool kKeepOff = kInt4 && kGroup > 32;
+  f32x4 off[kKeepOff ? S : 1][kKeepOff ? 128 / kGroup : 1];
+  auto load_activations = [&](const RowBlock& b) {
+    int r = min(b.lo + col, b.hi - 1);   // surplus rows repeat the last
+    if (p.a_rows) r = min(max(p.a_rows[r] / p.a_div, 0), p.A_rows - 1);
+    const uint16_t* ap = p.A + (size_t)r * K + 8 * q;
+    uint4 raw[S][4];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = (wave * S + s) * 128 + 32 * j;
+        raw[s][j] = make_uint4(0, 0, 0, 0);
+        if (k < K) raw[s][j] = *reinterpret_cast<const uint4*>(ap + k);
+      }
+    const uint32_t c136 = 0xc308c308u;
+    const bf16x8 b136 = as_bf16x8(make_uint4(c136, c136, c136, c136));
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (kInt4) raw[s][j] = order_int4(raw[s][j]);
+        // used here, so that the compiler waits for these loads here and not, with every direct
+        // load, in front of each item's products
+        asm volatile("" : "+v"(raw[s][j].x), "+v"(raw[s][j].y), "+v"(raw[s][j].z), "+v"(raw[s][j].w));
+        a[s][j] = as_bf16x8(raw[s][j]);
+        if constexpr (kKeepOff) {
+          f32x4& o = off[s][32 * j / kGroup];
+          if (32 * j % kGroup == 0) o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][j], b136, o, 0, 0, 0);
+        }
+      }
+  };
+
+  struct Cursor {
+    int block, tile;
+    RowBlock rows;
+  };
+  auto next = [&](Cursor& c) {
+    if (++c.tile < tiles) return;
+    c.tile = 0;
+    if (++c.block < rows_of.count()) c.rows = rows_of.find(c.block);
+  };
+  const int first_block = uniform(first / tiles);
+  Cursor load{first_block, first - first_block * tiles, rows_of.find(first_block)};
+  Cursor cur = load, prev = load;
+  for (int i = 0; i < min(n, slots - 1); ++i) {
+    issue(load.rows, load.tile, i);
+    next(load);
+  }
+  load_activations(cur.rows);
+  int slot = 0, next_slot = slots - 1;
+  // sums of an item, each wave's in turn to the front: rows * kRows outputs over the threads
+  auto finish = [&](const Cursor& c, int i) {
+    const int rows = c.rows.hi - c.rows.lo;
+    const int o = (int)(threadIdx.x + (W - i % W) * 64) % (W * 64);
+    if (o < rows * kRows) {
+      const int r = o / kRows, n_at = o % kRows;
+      auto sum = [&](int cc) {
+        float s = red[i & 1][0][r][cc];
+#pragma unroll
+        for (int v = 1; v < W; ++v) s += red[i & 1][v][r][cc];
+        return s;
+      };
+      float v = sum(n_at);
+      if constexpr (kSilu) v = silu_mul(v, sum(8 + n_at));
+      const int row = row0_of(c.tile) + n_at;
+      if (row >= c.tile * kRows && row < n_out) store(c.rows.lo + r, row, v);   // overlapped columns: the tile before
+    }
+  };
+  for (int i = 0; i < n; ++i) {
+    // loads of this item have landed; LDS is drained: everyone's reads of the previous slot and
+    // writes of sums are behind the barrier
+    wait_slices<Cfg::kLoads, Cfg::kMaxSlots - 2, true>(min(slots - 2, n - 1 - i));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (i + slots - 1 < n) {
+      issue(load.rows, load.tile, next_slot);
+      next(load);
+    }
+    next_slot = next_slot + 1 == slots ? 0 : next_slot + 1;
+    if (i > 0) finish(prev, i - 1);
+    const uint8_t* in = ring + slot * slot_bytes;
+    slot = slot + 1 == slots ? 0 : slot + 1;
+    // scales
+    uint32_t sc[kWords];
+    {
+      uint32_t shift = 0;   // bytes before the first scale (rows that are not swizzled)
+      if (scale_row % 16 != 0)
+        shift = (uint32_t)((reinterpret_cast<uintptr_t>(p.scales) +
+                            ((size_t)cur.rows.e * p.N + row0_of(cur.tile) + (wseg ? second : 0)) * scale_row) & 15);
+      uint32_t raw[kReads];
+      if constexpr (kInt4) {
+#pragma unroll
+        for (int w = 0; w < kReads; ++w)
+          raw[w] = *reinterpret_cast<const uint32_t*>(in + scale_from[w / kFromWords] + shift + 4 * (w % kFromWords));
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) sc[w] = raw[w] & scale_ok[w];   // past K: 0
+      } else {
+        const uint32_t odd = (scale_from[0] + shift) & 3;   // the same for every word
+#pragma unroll
+        for (int w = 0; w < kReads; ++w)
+          raw[w] = *reinterpret_cast<const uint32_t*>(in + ((scale_from[w] + shift) & ~3u));
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)   // past K: 2^0
+          sc[w] = (__builtin_amdgcn_alignbyte(raw[w + 1], raw[w], odd) & scale_ok[w]) | (0x7f7f7f7fu & ~scale_ok[w]);
+      }
+    }
+    // two sums, so that a product need not wait for the one before it
+    f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const uint4 v = *reinterpret_cast<const uint4*>(in + code_from[s]);
+      uint32_t c[4] = {v.x, v.y, v.z, v.w};
+      transpose4(c);
+      if constexpr (kInt4) {
+        uint32_t c136 = 0xc308c308u;
+        if constexpr (!kKeepOff) asm volatile("" : "+v"(c136));   // or the compiler keeps them after all
+        const bf16x8 b136 = as_bf16x8(make_uint4(c136, c136, c136, c136));
+        f32x4 d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (!kKeepOff)
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][j], b136, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+          else if (32 * j % kGroup == 0)
+            d = off[s][32 * j / kGroup];
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][j], as_bf16x8(unpack_int4(c[j])), d, 0, 0, 0);
+          if (32 * (j + 1) % kGroup == 0)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[j & 1][e] = fmaf(__uint_as_float(sc[s * (128 / kGroup) + 32 * j / kGroup]), d[e], acc[j & 1][e]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a[s][j], as_bf16x8(unpack_mxfp4(c[j], sc[s] >> (8 * j) & 0xff)), acc[j & 1], 0, 0, 0);
+      }
+    }
+    const int rows = cur.rows.hi - cur.rows.lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * q + e < rows) red[i & 1][wave][4 * q + e][col] = acc[0][e] + acc[1][e];
+    prev = cur;
+    next(cur);
+    if (cur.block != prev.block && i + 1 < n) load_activations(cur.rows);
+  }
+  __syncthreads();
+  finish(prev, n - 1);
+}
+
 // How a launch is cut: row tiles per row block by the rows an expert has on average, weight tiles
 // per workgroup by how many workgroups that leaves.
 constexpr int kMaxNT = FB_NT, kMinWg = FB_WG;
@@ -383,12 +720,41 @@ long long fourbit_workgroups(long long M_rows, int E, long long n_out, bool silu
   return fourbit_cut(M_rows, E, n_out, silu).workgroups;
 }
 
+// few rows per expert and a row of codes that eight waves of seven steps hold
+static bool fourbit_streams(long long M_rows, int E, long long K) {
+  return M_rows <= 8ll * E && K <= kStreamWaves * kStreamMaxS * 128;
+}
+
+template <bool kInt4, int kGroup, bool kSilu>
+static hipError_t launch_fourbit_stream(const FourbitArgs& a, hipStream_t stream) {
+  const int n_out = kSilu ? a.N / 2 : a.N, rows = kSilu ? 8 : 16;
+  const long long items = fourbit_blocks(a.M_rows, a.E, 16) * ((n_out + rows - 1) / rows);
+  const int steps = (a.K + 127) / 128;
+  const auto go = [&](auto s) {
+    constexpr int S = decltype(s)::value;
+    const unsigned grid = (unsigned)std::min<long long>(items, 256 * StreamCfg<kInt4, kGroup, S>::kPerCu);
+    hipLaunchKernelGGL((fourbit_stream_kernel<kInt4, kGroup, kSilu, S>), dim3(grid), dim3(kStreamWaves * 64), 0, stream, a);
+    return hipGetLastError();
+  };
+  switch ((steps + kStreamWaves - 1) / kStreamWaves) {
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 3: return go(std::integral_constant<int, 3>{});
+    case 4: return go(std::integral_constant<int, 4>{});
+    case 5: return go(std::integral_constant<int, 5>{});
+    case 6: return go(std::integral_constant<int, 6>{});
+    case 7: return go(std::integral_constant<int, 7>{});
+  }
+  return hipErrorInvalidValue;
+}
+
 template <bool kInt4, int kGroup, bool kSilu>
 static hipError_t launch_fourbit_s(const FourbitLaunch& p, hipStream_t stream) {
   const FourbitCut cut = fourbit_cut(p.M_rows, p.E, kSilu ? p.N / 2 : p.N, kSilu);
   const FourbitArgs a{static_cast<const uint16_t*>(p.A), p.a_rows, p.a_div, (int)p.a_total,
                       static_cast<const uint8_t*>(p.codes), p.scales, p.offsets, p.E, (int)p.M_rows, (int)p.N,
                       (int)p.K, p.C, p.c_f32};
+  if (fourbit_streams(p.M_rows, p.E, p.K)) return launch_fourbit_stream<kInt4, kGroup, kSilu>(a, stream);
   const dim3 grid((unsigned)cut.workgroups), block(kFbWaves * 64);
   const int lds = fourbit_lds(cut.MT, cut.NT, p.K, kStepScaleBytes<kInt4, kGroup>);
   constexpr int kPer = kSilu ? 2 : 1;   // weight tiles per output tile
