@@ -446,7 +446,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   const int items = rows_of.count() * tiles;
   const int share = uniform(items / (int)gridDim.x), extra = items - share * (int)gridDim.x;
   const int first = (int)blockIdx.x * share + min((int)blockIdx.x, extra);
-  const int n = share + ((int)blockIdx.x < extra ? 1 : 0);
+  const int n = uniform(share + ((int)blockIdx.x < extra ? 1 : 0));
   if (n == 0) return;
 
   // ---- this lane's part of the direct loads
@@ -576,12 +576,14 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
     RowBlock rows;
   };
   auto next = [&](Cursor& c) {
-    if (++c.tile < tiles) return;
+    c.tile = uniform(c.tile + 1);
+    if (c.tile < tiles) return;
     c.tile = 0;
-    if (++c.block < rows_of.count()) c.rows = rows_of.find(c.block);
+    c.block = uniform(c.block + 1);
+    if (c.block < rows_of.count()) c.rows = rows_of.find(c.block);
   };
   const int first_block = uniform(first / tiles);
-  Cursor load{first_block, first - first_block * tiles, rows_of.find(first_block)};
+  Cursor load{first_block, uniform(first - first_block * tiles), rows_of.find(first_block)};
   Cursor cur = load, prev = load;
   for (int i = 0; i < min(n, slots - 1); ++i) {
     issue(load.rows, load.tile, i);
