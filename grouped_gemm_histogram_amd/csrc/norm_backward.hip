@@ -16,16 +16,21 @@
 
 namespace moe {
 
+// waves of a block
+template <int W>
+constexpr int kNbWaves = W < 8 ? 8 : W;
+
 // dx may be dy or x
 template <typename T, bool kVec, int W, int C>
-__global__ __launch_bounds__(W < 4 ? 256 : W * 64) void norm_backward_kernel(
+__global__ __launch_bounds__(kNbWaves<W> * 64) void norm_backward_kernel(
     const T* dy, const T* x, long long T_rows, int H, const void* __restrict__ weight,
     int w_bf16, const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int rms, T* dx,
     float* __restrict__ part) {
   constexpr int EL = kRowEl<T>;
-  constexpr int kWaves = W < 4 ? 4 : W;
+  constexpr int kWaves = kNbWaves<W>;
   constexpr int kSlots = kWaves / W;
-  __shared__ float2 red[2 * kWaves];
+  __shared__ float red[2 * 2 * kWaves];
+  __shared__ float merge[kSlots > 1 ? kSlots / 2 * W * kWave : 1][kSlots > 1 ? C * EL + 1 : 1];   // a row a thread, odd
   const int wave = threadIdx.x >> 6;
   const int slot = wave / W;
   const int rl = (wave % W) * kWave + lane_id();   // lane within the row
@@ -77,8 +82,9 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void norm_backward_kernel(
         s2 = fmaf(g, xhat, s2);
       }
     }
-    row_sum2<W>(s1, s2, red, buf ^= 1, kWaves);
-    const float m1 = rms ? 0.0f : s1 * inv_h, m2 = s2 * inv_h;
+    float s[2] = {s1, s2};
+    row_sums<W>(s, red, buf ^= 1, kWaves);
+    const float m1 = rms ? 0.0f : s[0] * inv_h, m2 = s[1] * inv_h;
     if (t < T_rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -95,8 +101,30 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void norm_backward_kernel(
       }
     }
   }
-  if (part) {
-    float* pw = part + ((long long)blockIdx.x * kSlots + slot) * 2 * H;
+  if (!part) return;
+  // the slots' sums in a tree: the upper half of the slots left hands its sums to the lower
+  const int at = (slot * W + wave % W) * kWave + lane_id();   // thread of the block, by slot
+#pragma unroll
+  for (int half = kSlots / 2; half >= 1; half /= 2) {
+    auto exchange = [&](float (&v)[C][EL]) {
+      __syncthreads();
+      if (slot >= half && slot < 2 * half)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < EL; ++i) merge[at - half * W * kWave][c * EL + i] = v[c][i];
+      __syncthreads();
+      if (slot < half)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < EL; ++i) v[c][i] += merge[at][c * EL + i];
+    };
+    exchange(dw);
+    exchange(db);
+  }
+  if (slot == 0) {
+    float* pw = part + (long long)blockIdx.x * 2 * H;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = (c * W * kWave + rl) * EL;
@@ -140,8 +168,8 @@ __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float* __rest
   }
 }
 
-// row slots of a launch: as many as the rows can use, at most kPartRows
-constexpr int kPartRows = 512;
+// blocks of a launch, each with one row of partial sums
+constexpr int kPartRows = 256;
 
 template <typename T, bool kVec>
 struct NormBackwardLauncher {
@@ -149,18 +177,16 @@ struct NormBackwardLauncher {
   hipStream_t stream;
   template <int W, int C>
   hipError_t operator()() const {
-    constexpr int kWaves = W < 4 ? 4 : W;
-    constexpr int kSlots = kWaves / W;
-    const long long blocks = (p.T + kSlots - 1) / kSlots;
-    const unsigned grid = (unsigned)std::min<long long>(blocks, kPartRows / kSlots);
+    constexpr int kSlots = kNbWaves<W> / W;
+    const unsigned grid = (unsigned)std::min<long long>((p.T + kSlots - 1) / kSlots, kPartRows);
     const bool sums = p.dweight || p.dbias;
     if (p.T > 0)
-      hipLaunchKernelGGL((norm_backward_kernel<T, kVec, W, C>), dim3(grid), dim3(kWaves * kWave), 0, stream,
+      hipLaunchKernelGGL((norm_backward_kernel<T, kVec, W, C>), dim3(grid), dim3(kNbWaves<W> * kWave), 0, stream,
                          static_cast<const T*>(p.dy), static_cast<const T*>(p.x), p.T, p.H, p.weight, p.w_bf16,
                          p.mean, p.rstd, p.rms, static_cast<T*>(p.dx), sums ? p.part : nullptr);
     if (sums)
       hipLaunchKernelGGL(norm_grad_sum_kernel, dim3((2 * p.H + kWave - 1) / kWave), dim3(1024), 0, stream, p.part,
-                         (int)grid * kSlots, p.H, p.dweight, p.dbias, p.grad_bf16);
+                         (int)grid, p.H, p.dweight, p.dbias, p.grad_bf16);
     return hipGetLastError();
   }
 };
@@ -168,17 +194,17 @@ struct NormBackwardLauncher {
 template <typename T>
 static hipError_t launch_norm_backward_t(const NormBackwardLaunch& p, hipStream_t stream) {
   const int units = (p.H + kRowEl<T> - 1) / kRowEl<T>;
-  if (p.H % kRowEl<T> == 0) return dispatch_row(units, NormBackwardLauncher<T, true>{p, stream});
-  return dispatch_row(units, NormBackwardLauncher<T, false>{p, stream});
+  constexpr int kMaxC = 16 / kRowEl<T>;
+  if (p.H % kRowEl<T> == 0) return dispatch_row<kMaxC>(units, NormBackwardLauncher<T, true>{p, stream});
+  return dispatch_row<kMaxC>(units, NormBackwardLauncher<T, false>{p, stream});
 }
 
 hipError_t launch_norm_backward(const NormBackwardLaunch& p, hipStream_t stream) {
   return p.x_bf16 ? launch_norm_backward_t<uint16_t>(p, stream) : launch_norm_backward_t<float>(p, stream);
 }
 
-// partial rows: blocks * slots, at most the rows rounded up to whole blocks (four slots)
 size_t norm_backward_workspace_bytes(long long T, int H) {
-  return (size_t)std::min<long long>((T + 3) / 4 * 4, kPartRows) * 2 * H * sizeof(float);
+  return (size_t)std::min<long long>(T, kPartRows) * 2 * H * sizeof(float);
 }
 
 }  // namespace moe

@@ -5,6 +5,8 @@
 // element's alignment (H may be odd): global 16-byte loads and stores take any address.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace moe {
@@ -54,10 +56,15 @@ __device__ __forceinline__ uint4 chunk_from_f32(const float (&v)[kRowEl<T>]) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-template <typename T, bool kVec>
+// kNt: not kept in the caches
+template <typename T, bool kVec, bool kNt = false>
 __device__ __forceinline__ void store_chunk(T* p, const uint4& r, int nvalid) {
   if (kVec ? nvalid > 0 : nvalid >= kRowEl<T>) {
-    __builtin_memcpy(p, &r, 16);
+    typedef __attribute__((__vector_size__(16), __aligned__(2))) uint32_t AnyU32x4;
+    if constexpr (kNt)
+      __builtin_nontemporal_store(AnyU32x4{r.x, r.y, r.z, r.w}, reinterpret_cast<AnyU32x4*>(p));
+    else
+      __builtin_memcpy(p, &r, 16);
   } else if (!kVec && nvalid > 0) {
     T e[kRowEl<T>];
     __builtin_memcpy(e, &r, 16);
@@ -72,6 +79,17 @@ __device__ __forceinline__ void store_chunk(T* p, const uint4& r, int nvalid) {
 template <int n>
 __device__ __forceinline__ void load_params(const void* p, bool bf16, long long at, int nvalid, float fill,
                                             float (&v)[n]) {
+  if (p && nvalid >= n) {   // whole: n / 8 or n / 4 loads of 16 bytes (at least one of 8)
+    if (bf16) {
+      uint32_t u[n / 2];
+      __builtin_memcpy(u, static_cast<const uint16_t*>(p) + at, 2 * n);
+#pragma unroll
+      for (int i = 0; i < n; ++i) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    } else {
+      __builtin_memcpy(v, static_cast<const float*>(p) + at, 4 * n);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     float f = fill;
@@ -81,45 +99,63 @@ __device__ __forceinline__ void load_params(const void* p, bool bf16, long long 
   }
 }
 
-// Sums of a and b over the W waves of a row; every lane gets them.  red: 2 * waves-per-block
-// pairs of LDS; `buf` (0 or 1) alternates between consecutive calls, so that the barrier of the
-// call in between separates a buffer's readers from its next writers.
-template <int W>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float2* red, int buf, int nwaves) {
-  a = wave_sum(a);
-  b = wave_sum(b);
+// The sum over a row of 16 lanes of groups that repeat every `from` lanes: rotations, so that every
+// lane adds the same values pairwise in the same tree and gets the same bits.
+template <int from>
+__device__ __forceinline__ float lanes16_sum(float v) {
+  auto rotated = [](float x, auto by) {   // row_ror:by
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + decltype(by)::value, 0xf, 0xf, false));
+  };
+  if constexpr (from >= 16) v += rotated(v, std::integral_constant<int, 8>{});
+  if constexpr (from >= 8) v += rotated(v, std::integral_constant<int, 4>{});
+  if constexpr (from >= 4) v += rotated(v, std::integral_constant<int, 2>{});
+  if constexpr (from >= 2) v += rotated(v, std::integral_constant<int, 1>{});
+  return v;
+}
+
+// The sum over the 64 lanes, in every lane (the same bits): within rows of 16 lanes, then across
+// them by exchanging rows, without a trip through LDS.
+__device__ __forceinline__ float wave_total(float v) {
+  v = lanes16_sum<16>(v);
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// Sums of N values over the W waves of a row; every lane gets them.  red: 2 * N floats of LDS per
+// wave of the block; `buf` (0 or 1) alternates between consecutive calls, so that the barrier of
+// the call in between separates a buffer's readers from its next writers.
+template <int W, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* red, int buf, int nwaves) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_total(v[i]);
   if constexpr (W > 1) {
     const int wave = threadIdx.x >> 6;
-    if (lane_id() == 0) red[buf * nwaves + wave] = make_float2(a, b);
-    __syncthreads();
-    a = 0.0f;
-    b = 0.0f;
+    float* mine = red + buf * nwaves * N;
+    if (lane_id() == 0)
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 s = red[buf * nwaves + (wave / W) * W + i];
-      a += s.x;
-      b += s.y;
-    }
+      for (int i = 0; i < N; ++i) mine[wave * N + i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lanes16_sum<W>(mine[((wave / W) * W + lane_id() % W) * N + i]);
   }
 }
 
-// waves per row and chunks per lane for `units` 16-byte units of a row: the fewest waves that
-// hold it in at most four chunks a lane (eight at sixteen waves)
-template <typename F>
-inline hipError_t dispatch_row(int units, F&& f) {
-  const int u = (units + kWave - 1) / kWave;
-  if (u <= 1) return f.template operator()<1, 1>();
-  if (u <= 2) return f.template operator()<1, 2>();
-  if (u <= 3) return f.template operator()<1, 3>();
-  if (u <= 4) return f.template operator()<1, 4>();
-  if (u <= 6) return f.template operator()<2, 3>();
-  if (u <= 8) return f.template operator()<2, 4>();
-  if (u <= 12) return f.template operator()<4, 3>();
-  if (u <= 16) return f.template operator()<4, 4>();
-  if (u <= 24) return f.template operator()<8, 3>();
-  if (u <= 32) return f.template operator()<8, 4>();
-  if (u <= 64) return f.template operator()<16, 4>();
-  return f.template operator()<16, 8>();
+// Waves per row and chunks per lane for `units` 16-byte units of a row: the fewest waves that
+// hold it in at most kMaxC chunks a lane, or sixteen waves.
+template <int kMaxC, int W, int C, typename F>
+hipError_t dispatch_row_from(int u, F&& f) {
+  if (u <= W * C) return f.template operator()<W, C>();
+  if constexpr (C < kMaxC || (W == 16 && C < 8))
+    return dispatch_row_from<kMaxC, W, C + 1>(u, f);
+  else if constexpr (W < 16)
+    return dispatch_row_from<kMaxC, 2 * W, C / 2 + 1>(u, f);
+  return hipErrorInvalidValue;
+}
+template <int kMaxC, typename F>
+hipError_t dispatch_row(int units, F&& f) {
+  return dispatch_row_from<kMaxC, 1, 1>((units + kWave - 1) / kWave, f);
 }
 
 }  // namespace moe
