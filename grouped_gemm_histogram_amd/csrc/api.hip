@@ -766,9 +766,6 @@ bool fourbit_sizes_ok(long long T, long long H, long long I, int E, int k) {
          H <= kMaxRows && 2 * I <= kMaxRows && T <= kMaxRows && T * k <= kMaxRows;
 }
 
-// a launch's grid has 256-thread workgroups and under 2^32 threads
-constexpr long long kMaxWorkgroups = (1ll << 24) - 1;
-
 moe_status_t check_dropout(double p, const uint64_t* rng) {
   MOE_REQUIRE(p >= 0.0 && p <= 1.0, "p=%g outside [0, 1]", p);
   MOE_REQUIRE(rng, "rng is null");
@@ -829,8 +826,9 @@ moe_status_t moe_grouped_matvec_fourbit(const void* A, int64_t A_rows, const int
   MOE_REQUIRE(A && codes && scales && offsets && C, "null pointer argument");
   MOE_REQUIRE(aligned16(A) && aligned16(codes) && aligned16(scales) && aligned16(C),
               "A, codes, scales and C must be 16-byte aligned");
-  if (moe::fourbit_workgroups(M_rows, E, silu ? N / 2 : N, silu) > kMaxWorkgroups)
-    return fail(MOE_ERR_UNSUPPORTED, "%lld rows of %lld columns exceed one launch", (long long)M_rows, (long long)N);
+  if (!moe::fourbit_fits(M_rows, E, N, K, format == MOE_INT4, group, silu))
+    return fail(MOE_ERR_UNSUPPORTED, "%lld rows of %lld columns of %lld channels exceed one launch", (long long)M_rows,
+                (long long)N, (long long)K);
   moe::FourbitLaunch p{};
   p.A = A;
   p.a_rows = gather_rows;
@@ -875,8 +873,10 @@ moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, cons
     MOE_REQUIRE(aligned16(x) && aligned16(w13_codes) && aligned16(w13_scales) && aligned16(w2_codes) &&
                     aligned16(w2_scales) && aligned16(out),
                 "x, weights, scales and out must be 16-byte aligned");
-    if (std::max(moe::fourbit_workgroups(R, E, I, true), moe::fourbit_workgroups(R, E, H, false)) > kMaxWorkgroups)
-      return fail(MOE_ERR_UNSUPPORTED, "%lld routed rows exceed one launch", R);
+    const bool int4 = format == MOE_INT4;
+    if (!moe::fourbit_fits(R, E, 2 * I, H, int4, group, true) || !moe::fourbit_fits(R, E, H, I, int4, group, false))
+      return fail(MOE_ERR_UNSUPPORTED, "%lld routed rows, H=%lld, I=%lld exceed one launch", R, (long long)H,
+                  (long long)I);
   }
   const FourbitLayout L = fourbit_layout(T, H, I, E, k);
   if (!workspace || workspace_bytes < L.total)

@@ -20,6 +20,8 @@
 // of one scale.  The offset 136 leaves through a second MFMA with the constant weight -136,
 // shared by gate and up.  Its terms are at most 17 times the true ones, 2^-24 each.
 
+#include <limits.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -141,12 +143,7 @@ struct FourbitArgs {
   bool c_f32;
 };
 
-#ifndef FB_WAVES
-#define FB_WAVES 4
-#define FB_NT 4
-#define FB_WG 512
-#endif
-constexpr int kFbWaves = FB_WAVES;
+constexpr int kFbWaves = 4;
 constexpr int kStep = 256;   // channels of a step: 128 bytes of a weight row, one cache line
 
 // Two registers of a wave, each 8 weight rows x 128 bytes (lane 16 q + c: row c % 8, 16-byte piece
@@ -690,47 +687,49 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   finish(prev, n - 1);
 }
 
-// How a launch is cut: row tiles per row block by the rows an expert has on average, weight tiles
-// per workgroup by how many workgroups that leaves.
-constexpr int kMaxNT = FB_NT, kMinWg = FB_WG;
-
+// How a launch is cut.  stream: the streaming kernel, 16 rows a block.  Otherwise MT row tiles of 16
+// and NT weight tiles a workgroup.
 struct FourbitCut {
+  bool stream;
   int MT, NT;
-  long long workgroups;
+  int lds;                // dynamic LDS bytes of a workgroup
+  long long workgroups;   // streaming: items
 };
 
-static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, bool silu) {
-  FourbitCut c;
-  c.MT = M_rows <= 8ll * E ? 1 : M_rows <= 24ll * E ? 2 : 4;
-  const long long blocks = fourbit_blocks(M_rows, E, 16 * c.MT);
-  const auto wgs = [&](int nt) { return blocks * ((n_out + 16 * nt - 1) / (16 * nt)); };
-  int nt = c.MT == 4 ? 1 : silu || c.MT == 2 ? kMaxNT / 2 : kMaxNT;   // output tiles
-  if (c.MT == 2 && silu) nt = kMaxNT / 4;
-  if (c.MT == 1)
-    while (nt > 1 && wgs(nt) < kMinWg) nt /= 2;
-  c.NT = silu ? 2 * nt : nt;
-  c.workgroups = wgs(nt);
+constexpr int kMaxLds = 64 << 10;   // dynamic LDS of a launch
+#ifndef FB_T1
+#define FB_T1 8
+#define FB_T2 24
+#endif
+
+static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, long long K, int step_bytes, bool silu) {
+  FourbitCut c{};
+  if (M_rows <= (long long)FB_T1 * E && K <= kStreamWaves * kStreamMaxS * 128) {
+    c.stream = true;
+    c.workgroups = fourbit_blocks(M_rows, E, 16) * ((n_out + (silu ? 7 : 15)) / (silu ? 8 : 16));
+    return c;
+  }
+  c.MT = M_rows <= 8ll * E ? 1 : M_rows <= (long long)FB_T2 * E ? 2 : 4;
+  const int per = silu ? 2 : 1;   // weight tiles of an output tile
+  // the scales of the tiles' rows; afterwards the waves' sums
+  const auto lds = [&](int nt) {
+    return std::max<long long>((long long)nt * 16 * scale_row_bytes(K, step_bytes), kFbWaves * nt * c.MT * 1024);
+  };
+  c.NT = std::max(4 / c.MT, per);
+  while (c.NT > per && lds(c.NT) > kMaxLds) c.NT /= 2;
+  c.lds = (int)std::min<long long>(lds(c.NT), INT_MAX);
+  c.workgroups = fourbit_blocks(M_rows, E, 16 * c.MT) * ((n_out + 16 * (c.NT / per) - 1) / (16 * (c.NT / per)));
   return c;
 }
 
-// the scales of the tiles' rows; afterwards the waves' sums
-static int fourbit_lds(int MT, int NT, long long K, int step_bytes) {
-  return std::max(NT * 16 * scale_row_bytes(K, step_bytes), kFbWaves * NT * MT * 1024);
-}
-
-long long fourbit_workgroups(long long M_rows, int E, long long n_out, bool silu) {
-  return fourbit_cut(M_rows, E, n_out, silu).workgroups;
-}
-
-// few rows per expert and a row of codes that eight waves of seven steps hold
-static bool fourbit_streams(long long M_rows, int E, long long K) {
-  return M_rows <= 8ll * E && K <= kStreamWaves * kStreamMaxS * 128;
+bool fourbit_fits(long long M_rows, int E, long long N, long long K, bool int4, int group, bool silu) {
+  const FourbitCut c = fourbit_cut(M_rows, E, silu ? N / 2 : N, K, kStep / group * (int4 ? 4 : 1), silu);
+  // a grid holds fewer than 2^32 threads; items are counted in 32 bits
+  return c.stream ? c.workgroups <= INT_MAX : c.workgroups < (1ll << 24) && c.lds <= kMaxLds;
 }
 
 template <bool kInt4, int kGroup, bool kSilu>
-static hipError_t launch_fourbit_stream(const FourbitArgs& a, hipStream_t stream) {
-  const int n_out = kSilu ? a.N / 2 : a.N, rows = kSilu ? 8 : 16;
-  const long long items = fourbit_blocks(a.M_rows, a.E, 16) * ((n_out + rows - 1) / rows);
+static hipError_t launch_fourbit_stream(const FourbitArgs& a, long long items, hipStream_t stream) {
   const int steps = (a.K + 127) / 128;
   const auto go = [&](auto s) {
     constexpr int S = decltype(s)::value;
@@ -752,25 +751,24 @@ static hipError_t launch_fourbit_stream(const FourbitArgs& a, hipStream_t stream
 
 template <bool kInt4, int kGroup, bool kSilu>
 static hipError_t launch_fourbit_s(const FourbitLaunch& p, hipStream_t stream) {
-  const FourbitCut cut = fourbit_cut(p.M_rows, p.E, kSilu ? p.N / 2 : p.N, kSilu);
+  const FourbitCut cut =
+      fourbit_cut(p.M_rows, p.E, kSilu ? p.N / 2 : p.N, p.K, kStepScaleBytes<kInt4, kGroup>, kSilu);
   const FourbitArgs a{static_cast<const uint16_t*>(p.A), p.a_rows, p.a_div, (int)p.a_total,
                       static_cast<const uint8_t*>(p.codes), p.scales, p.offsets, p.E, (int)p.M_rows, (int)p.N,
                       (int)p.K, p.C, p.c_f32};
-  if (fourbit_streams(p.M_rows, p.E, p.K)) return launch_fourbit_stream<kInt4, kGroup, kSilu>(a, stream);
+  if (cut.stream) return launch_fourbit_stream<kInt4, kGroup, kSilu>(a, cut.workgroups, stream);
   const dim3 grid((unsigned)cut.workgroups), block(kFbWaves * 64);
-  const int lds = fourbit_lds(cut.MT, cut.NT, p.K, kStepScaleBytes<kInt4, kGroup>);
-  constexpr int kPer = kSilu ? 2 : 1;   // weight tiles per output tile
-#define MOE_FOURBIT(MT_, NT_)                                                                             \
-  if (cut.MT == MT_ && cut.NT == NT_ * kPer) {                                                            \
-    hipLaunchKernelGGL((fourbit_kernel<kInt4, kGroup, kSilu, MT_, NT_ * kPer>), grid, block, lds, stream, a); \
-    return hipGetLastError();                                                                               \
+#define MOE_FOURBIT(MT_, NT_)                                                                              \
+  if (cut.MT == MT_ && cut.NT == NT_) {                                                                   \
+    hipLaunchKernelGGL((fourbit_kernel<kInt4, kGroup, kSilu, MT_, NT_>), grid, block, cut.lds, stream, a); \
+    return hipGetLastError();                                                                             \
   }
-  MOE_FOURBIT(1, 1)
-  if constexpr (kMaxNT >= 4 || !kSilu) { MOE_FOURBIT(1, 2) }
-  if constexpr (kMaxNT / kPer >= 4) { MOE_FOURBIT(1, 4) }
-  if constexpr (kMaxNT / kPer >= 8) { MOE_FOURBIT(1, 8) }
-  MOE_FOURBIT(2, (kMaxNT / 2 / kPer))
-  MOE_FOURBIT(4, 1)
+  if constexpr (!kSilu) { MOE_FOURBIT(1, 1) }
+  MOE_FOURBIT(1, 2)
+  MOE_FOURBIT(1, 4)
+  if constexpr (!kSilu) { MOE_FOURBIT(2, 1) }
+  MOE_FOURBIT(2, 2)
+  MOE_FOURBIT(4, (kSilu ? 2 : 1))
 #undef MOE_FOURBIT
   return hipErrorInvalidValue;
 }

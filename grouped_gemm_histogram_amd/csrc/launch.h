@@ -187,8 +187,8 @@ struct FourbitLaunch {
   bool c_f32;                  // else bf16
 };
 hipError_t launch_fourbit(const FourbitLaunch& p, hipStream_t stream);
-// workgroups of 256 threads of a launch (a grid holds fewer than 2^32 threads)
-long long fourbit_workgroups(long long M_rows, int E, long long n_out, bool silu);
+// whether a launch of these sizes fits its grid and LDS
+bool fourbit_fits(long long M_rows, int E, long long N, long long K, bool int4, int group, bool silu);
 // n values of whole groups -> codes and scales
 hipError_t launch_quantize_fourbit(const void* w, bool bf16, long long n, bool int4, int group, void* codes,
                                    void* scales, hipStream_t stream);

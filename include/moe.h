@@ -384,7 +384,9 @@ moe_status_t moe_backward(const void* x, const void* w13, const float* w13_scale
  *              [E, N, K/32], group 32.  e2m1 codes are sign, two exponent bits,
  *              one mantissa bit: 0 0.5 1 1.5 2 3 4 6 and their negatives.
  *
- * K is a multiple of 32 and of group.
+ * K is a multiple of 32 and of group.  Codes and scales are 16-byte aligned and
+ * are read in whole aligned 16-byte units: the last unit's bytes past the last
+ * scale are read as well (and not used).
  */
 
 /*
@@ -409,10 +411,14 @@ moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E,
  *   for p in [offsets[e], offsets[e+1]):
  *       acc[p, n] = sum_k A[row(p), k] * value(codes[e, n, k])
  *
- *   A            bf16 [A_rows, K], |A| < 2^120 for MOE_INT4.  row(p) = p
- *                (A_rows >= M_rows), or with gather_rows (device int32
- *                [M_rows]) gather_rows[p] / gather_div clamped into A.
- *   codes, scales  4-bit weights [E, N, K], see above.
+ *   A            bf16 [A_rows, K].  row(p) = p (A_rows >= M_rows), or with
+ *                gather_rows (device int32 [M_rows]) gather_rows[p] /
+ *                gather_div clamped into A.  MOE_INT4 needs |A| < 2^120: a row
+ *                with a larger or infinite entry may come out as NaN.
+ *   codes, scales  4-bit weights [E, N, K], see above; one expert's codes span
+ *                under 2 GiB.  K up to 16128 for int4 groups of 32, 32512 for groups
+ *                of 64, 65280 otherwise; beyond, MOE_ERR_UNSUPPORTED where a
+ *                workgroup's scales do not fit in LDS.
  *   offsets      device int32 [E+1], read on the device.
  *   epi          as for moe_grouped_gemm (SiLU*up: N even, N_out = N/2).
  *   C            [M_rows, N_out] of c_dtype (MOE_F32 or MOE_BF16), no
@@ -423,7 +429,8 @@ moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E,
  * expert (64 where the launch has more than 8 rows per expert on average), so
  * with many rows per expert moe_grouped_gemm on bf16 weights is faster.
  * Accumulation is f32, C is rounded once.  mxfp4 values are taken as bf16
- * (exact unless they leave bf16's range); int4 values are not rounded at all.
+ * (exact while they are normal bf16 numbers); int4 values are not rounded at
+ * all.
  */
 moe_status_t moe_grouped_matvec_fourbit(const void* A, int64_t A_rows, const int32_t* gather_rows,
                                         int32_t gather_div, const void* codes, const void* scales,

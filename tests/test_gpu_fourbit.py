@@ -170,6 +170,41 @@ def test_matvec_random(fmt, group, silu, N, K):
     assert torch.equal(buf, b16) and (buf[off[-1]:] == 0).all()
 
 
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("counts", [[2, 0, 1], [9, 12, 5], [30, 41, 17]])
+@pytest.mark.parametrize("silu", [False, True])
+def test_matvec_long_rows_exact(fmt, group, counts, silu):
+    """Channels past what the streaming kernel holds (7168), and that many exactly, at few, some and many
+    rows per expert."""
+    import grouped_gemm_histogram_amd as g
+    off, M = offsets_of(counts, 1)
+    for K in (7168, 7296, 14336):
+        say(f"matvec long {fmt} {group} counts={counts} silu={silu} K={K}")
+        codes, scales = weights(3, 34, K, fmt, group, K, exact=True)
+        a = torch.randint(-2, 3, (M, K), generator=gen(6)).to(torch.bfloat16)
+        ref, tol = reference(host(a), codes, scales, off, silu, exact=True)
+        out = g.grouped_matvec_fourbit(a.to(DEV), codes.to(DEV), scales.to(DEV),
+                                       torch.from_numpy(off).to(torch.int32).to(DEV), "silu_mul" if silu else "none",
+                                       out_dtype=torch.float32)
+        assert (np.abs(host(out) - ref) <= tol).all()
+
+
+def test_matvec_longest_rows_and_beyond():
+    import grouped_gemm_histogram_amd as g
+    off = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    for fmt, group, K in (("int4", 32, 16128), ("int4", 64, 32512), ("int4", 128, 65280), ("mxfp4", 32, 65280)):
+        codes, scales = weights(1, 4, K, fmt, group, K, exact=True)
+        a = (torch.arange(K) % 97 == 0).to(torch.bfloat16)[None]      # few ones: sums stay exact
+        ref, tol = reference(host(a), codes, scales, np.array([0, 1]), True, exact=True)
+        out = g.grouped_matvec_fourbit(a.to(DEV), codes.to(DEV), scales.to(DEV), off, "silu_mul",
+                                       out_dtype=torch.float32)
+        assert (np.abs(host(out) - ref) <= tol).all(), fmt
+        long = torch.zeros(1, 2 * K + 512, dtype=torch.bfloat16, device=DEV)
+        codes, scales = (t.to(DEV) for t in weights(1, 4, 2 * K + 512, fmt, group, 1))
+        with pytest.raises(RuntimeError, match="MOE_ERR_UNSUPPORTED"):
+            g.grouped_matvec_fourbit(long, codes, scales, off, "silu_mul")
+
+
 def test_matvec_same_row_many_times_and_bad_maps():
     """A row map may repeat rows; entries outside A are clamped into it."""
     import grouped_gemm_histogram_amd as g
