@@ -78,7 +78,7 @@ __device__ __forceinline__ uint4 unpack_mxfp4(uint32_t v, uint32_t e8m0) {
   return r;
 }
 
-// The row blocks of a launch: every expert's rows in blocks of BM, expert by expert.  Each lane keeps
+// The row blocks of a launch: every expert's rows in blocks of 16, expert by expert.  Each lane keeps
 // the running count of its consecutive experts' blocks; all 64 lanes take part in each call.
 struct RowBlock {
   int e, lo, hi;   // rows [lo, hi) of expert e
@@ -89,14 +89,15 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 
 struct RowBlocks {
   const int* offsets;
-  int E, M_rows, BM, per;
+  int E, M_rows, per;
+  static constexpr int BM = 16;
   int lo0, hi0, mine, incl;
 
   __device__ __forceinline__ int at(int e) const { return min(max(offsets[min(e, E)], 0), M_rows); }
   __device__ __forceinline__ int blocks(int lo, int hi) const { return max(hi - lo + BM - 1, 0) / BM; }
 
-  __device__ __forceinline__ RowBlocks(const int* offsets_, int E_, int M_rows_, int BM_)
-      : offsets(offsets_), E(E_), M_rows(M_rows_), BM(BM_), per((E_ + kWave - 1) / kWave) {
+  __device__ __forceinline__ RowBlocks(const int* offsets_, int E_, int M_rows_)
+      : offsets(offsets_), E(E_), M_rows(M_rows_), per((E_ + kWave - 1) / kWave) {
     const int lane = lane_id();
     lo0 = at(lane * per);
     mine = 0;
@@ -185,11 +186,11 @@ __device__ __forceinline__ void stage_scales(const uint8_t* __restrict__ scales,
   }
 }
 
-// kGroup: channels per scale (mxfp4: 32).  MT row tiles, NT weight tiles of 16 rows (with SiLU * up
-// the even ones are gate and the odd ones up).
-template <bool kInt4, int kGroup, bool kSilu, int MT, int NT>
+// Long weight rows: blocks of 16 rows of an expert, NT weight tiles of 16 rows (with SiLU * up the even
+// ones are gate and the odd ones up).  kGroup: channels per scale (mxfp4: 32).
+template <bool kInt4, int kGroup, bool kSilu, int NT>
 __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p) {
-  constexpr int BM = 16 * MT;
+  constexpr int BM = 16;
   constexpr int kCols = (kSilu ? NT / 2 : NT) * 16;   // output columns
   constexpr int kScaleBytes = kInt4 ? 4 : 1;
   constexpr int kScaleWords = kStepScaleBytes<kInt4, kGroup> / 4;   // scales of a row per step
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
   const int n_out = kSilu ? p.N / 2 : p.N;
   const int groups = (n_out + kCols - 1) / kCols;
   const int block = uniform(blockIdx.x / groups), n0 = ((int)blockIdx.x - block * groups) * kCols;
-  const RowBlocks rows_of(p.offsets, p.E, p.M_rows, BM);
+  const RowBlocks rows_of(p.offsets, p.E, p.M_rows);
   const int past = block - rows_of.count();
   RowBlock blk;
   if (past < 0) {
@@ -236,18 +237,12 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
 #pragma unroll
     for (int h = 0; h < 2; ++h) wat[t][h] = wrow(t, (col & 7) + 8 * h) * (uint32_t)(K / 2) + 16 * piece;
   }
-  const uint16_t* ap[MT];
+  int arow = min(blk.lo + col, blk.hi - 1);   // surplus rows repeat the last
+  if (p.a_rows) arow = min(max(p.a_rows[arow] / p.a_div, 0), p.A_rows - 1);
+  const uint16_t* ap = p.A + (size_t)arow * K;
+  f32x4 acc[NT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    int r = min(blk.lo + m * 16 + col, blk.hi - 1);
-    if (p.a_rows) r = min(max(p.a_rows[r] / p.a_div, 0), p.A_rows - 1);
-    ap[m] = p.A + (size_t)r * K;
-  }
-  f32x4 acc[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   struct Weights {
     uint4 c[2];
@@ -261,7 +256,7 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
       w.c[h] = make_uint4(v[0], v[1], v[2], v[3]);
     }
   };
-  uint4 a[MT][8];
+  uint4 a[8];
   const int scale_stride = scale_row_bytes(K, 4 * kScaleWords);
   auto multiply = [&](int k, int t, const Weights& w) {
     uint32_t c[2][4] = {{w.c[0].x, w.c[0].y, w.c[0].z, w.c[0].w}, {w.c[1].x, w.c[1].y, w.c[1].z, w.c[1].w}};
@@ -279,28 +274,21 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
       uint32_t c136 = 0xc308c308u;
       asm volatile("" : "+v"(c136));
       const bf16x8 b136 = as_bf16x8(make_uint4(c136, c136, c136, c136));
-      f32x4 d[MT];
+      f32x4 d;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bf16x8 b = as_bf16x8(unpack_int4(c[j >> 2][j & 3]));
+        if (32 * j % kGroup == 0) d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), b136, d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), as_bf16x8(unpack_int4(c[j >> 2][j & 3])), d, 0, 0, 0);
+        if (32 * (j + 1) % kGroup == 0)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (32 * j % kGroup == 0) d[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m][j]), b136, d[m], 0, 0, 0);
-          d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m][j]), b, d[m], 0, 0, 0);
-          if (32 * (j + 1) % kGroup == 0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(__uint_as_float(s[32 * j / kGroup]), d[m][i], acc[m][t][i]);
-        }
+          for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(__uint_as_float(s[32 * j / kGroup]), d[i], acc[t][i]);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bf16x8 b = as_bf16x8(unpack_mxfp4(c[j >> 2][j & 3], s[j >> 2] >> (8 * (j & 3)) & 0xff));
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m][j]), b, acc[m][t], 0, 0, 0);
-      }
+      for (int j = 0; j < 8; ++j)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            as_bf16x8(a[j]), as_bf16x8(unpack_mxfp4(c[j >> 2][j & 3], s[j >> 2] >> (8 * (j & 3)) & 0xff)), acc[t], 0, 0, 0);
     }
   };
   // every tile's weights of a step are in flight at once; a tile's next ones are asked for as
@@ -315,13 +303,11 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
   for (int k = wave * kStep; k < K; k += kFbWaves * kStep) {
     // MFMA j has channels 32 j + 8 q onwards of the step; channels past K are zero
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a[m][j] = make_uint4(0, 0, 0, 0);
-        if (k + 32 * j < K) a[m][j] = *reinterpret_cast<const uint4*>(ap[m] + k + 32 * j + 8 * q);
-        if constexpr (kInt4) a[m][j] = order_int4(a[m][j]);
-      }
+    for (int j = 0; j < 8; ++j) {
+      a[j] = make_uint4(0, 0, 0, 0);
+      if (k + 32 * j < K) a[j] = *reinterpret_cast<const uint4*>(ap + k + 32 * j + 8 * q);
+      if constexpr (kInt4) a[j] = order_int4(a[j]);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       multiply(k, t, w[t]);
@@ -334,12 +320,10 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
   float* red = reinterpret_cast<float*>(shared);
   auto at = [&](int v, int t, int r, int c) { return ((v * NT + t) * BM + r) * 16 + c; };
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (m * 16 + 4 * q + i < rows) red[at(wave, t, m * 16 + 4 * q + i, col)] = acc[m][t][i];
+    for (int i = 0; i < 4; ++i)
+      if (4 * q + i < rows) red[at(wave, t, 4 * q + i, col)] = acc[t][i];
   __syncthreads();
   for (int i = threadIdx.x; i < rows * kCols; i += kFbWaves * 64) {
     const int r = i / kCols, c = i % kCols;
@@ -358,8 +342,8 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
 }
 
 // row blocks: at most one partial block per expert that has rows, and one of rows without an expert
-static long long fourbit_blocks(long long M_rows, int E, int BM) {
-  return std::min<long long>(M_rows, M_rows / BM + std::min<long long>(E, M_rows) + 1);
+static long long fourbit_blocks(long long M_rows, int E) {
+  return std::min<long long>(M_rows, M_rows / 16 + std::min<long long>(E, M_rows) + 1);
 }
 
 // ---------------------------------------------------------------- few rows per expert: streaming
@@ -376,7 +360,16 @@ static long long fourbit_blocks(long long M_rows, int E, int BM) {
 // 16 lanes that read one piece of 16 rows hit different banks.
 
 constexpr int kStreamWaves = 8;
-constexpr int kStreamMaxS = 7;
+// steps a wave can hold activations for without spilling a register
+constexpr int stream_max_steps(bool int4, int group) { return int4 && group == 32 ? 5 : 7; }
+
+// the sum over the four rows of 16 lanes, in every lane
+__device__ __forceinline__ float quads_total(float v) {
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
 
 // 16-byte pieces of a row of `pieces` are stored at piece ^ row_swizzle(pieces, row), row < 16: with
 // G the largest power of two (to 16) in `pieces`, rows row + 16 / G start in the same bank, and
@@ -401,8 +394,9 @@ struct StreamCfg {
   static constexpr int kScaleLoads = (2 * kScaleKb + W - 1) / W;   // a wave's per item
   static constexpr int kLoads = S + kScaleLoads;
   static constexpr int kFixedKb = 2 * W + 1;   // two sets of sums, and a place for surplus loads
-  // two workgroups per CU where two slots each fit, else one
-  static constexpr int kPerCu = 2 * (2 * kSlotKb + kFixedKb) <= 160 ? 2 : 1;
+  // two workgroups per CU where two slots each fit in LDS and the loop in 128 registers (a spilled
+  // register's reload would wait for the direct loads before it), else one
+  static constexpr int kPerCu = 2 * (2 * kSlotKb + kFixedKb) <= 160 && S <= (kInt4 && kGroup == 32 ? 2 : 3) ? 2 : 1;
   static constexpr int kRingKb = 160 / kPerCu - kFixedKb;
   static constexpr int kMaxSlots = std::min(8, 63 / kLoads + 2);   // vmcnt counts to 63
   static_assert(kRingKb >= 2 * kSlotKb, "ring");
@@ -414,8 +408,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   using Cfg = StreamCfg<kInt4, kGroup, S>;
   constexpr int W = kStreamWaves;
   constexpr int kRows = kSilu ? 8 : 16;   // output columns of an item
-  constexpr int kWords = kInt4 ? S * (128 / kGroup) : S;   // words of scales a lane needs per item
-  constexpr int kReads = kInt4 ? kWords : kWords + 1;      // mxfp4's start at any byte
+  constexpr int kGroups = S * 128 / kGroup, kSums = kInt4 ? (kGroups + 3) / 4 : 1;
   __shared__ __align__(16) uint8_t ring[Cfg::kRingKb * 1024];
   __shared__ __align__(16) uint8_t spare[1024];
   __shared__ float red[2][W][16][16];
@@ -431,7 +424,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
     else
       static_cast<uint16_t*>(p.C)[at] = f32_to_bf16_bits(v);
   };
-  const RowBlocks rows_of(p.offsets, p.E, p.M_rows, 16);
+  const RowBlocks rows_of(p.offsets, p.E, p.M_rows);
   // rows without an expert are zero
   {
     const int V = rows_of.at(p.E);
@@ -516,7 +509,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
     code_from[s] = wseg * code_kb * 1024 + wr * row_bytes + ((piece ^ row_swizzle(pieces, col)) << 4);
   }
   // int4: where a step's scales start (they lie in one 16-byte piece); mxfp4: each word
-  constexpr int kFrom = kInt4 ? S : kReads, kFromWords = kInt4 ? 128 / kGroup : 1;
+  constexpr int kFrom = kInt4 ? S : S + 1, kFromWords = kInt4 ? 128 / kGroup : 1;   // mxfp4's may start inside a word
   int scale_from[kFrom];
   const int scale_swz = scale_row % 16 == 0 ? row_swizzle(scale_pieces, col) : 0;
   const int scale_first = wave * (S * 128 / kGroup) * Cfg::kScaleBytes;   // byte of a row's scales
@@ -525,17 +518,27 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
     const int b = scale_first + 4 * kFromWords * i;
     scale_from[i] = scale_base + wseg * scale_kb * 1024 + wr * scale_row + (((b >> 4) ^ scale_swz) << 4) + (b & 15);
   }
-  uint32_t scale_ok[kWords];   // bits of the words that are scales of channels below K
+  // int4: this lane's scales as the offsets' second operand, group 4 i + q; groups of 32: word q of step i
+  int sum_from[kInt4 && kGroup > 32 ? kSums : 1];
+  if constexpr (kInt4 && kGroup > 32) {
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    const int there = scale_row - scale_first - 4 * i;
-    scale_ok[i] = there >= 4 ? ~0u : there <= 0 ? 0u : (1u << (8 * there)) - 1;
+    for (int i = 0; i < kSums; ++i) {
+      const int b = scale_first + 4 * min(4 * i + q, kGroups - 1);
+      sum_from[i] = scale_base + wseg * scale_kb * 1024 + wr * scale_row + (((b >> 4) ^ scale_swz) << 4) + (b & 15);
+    }
+  }
+  uint32_t scale_ok[kInt4 ? 1 : S];   // mxfp4: bits of a step's word that are scales of channels below K
+  if constexpr (!kInt4) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int there = scale_row - scale_first - 4 * s;
+      scale_ok[s] = there >= 4 ? ~0u : there <= 0 ? 0u : (1u << (8 * there)) - 1;
+    }
   }
   bf16x8 a[S][4];
-  // int4: -136 times the sum of each group's activations, kept with the activations; groups of 32
-  // would take as many registers as those, so their offsets are made again for each item
-  constexpr bool kKeepOff = kInt4 && kGroup > 32;
-  f32x4 off[kKeepOff ? S : 1][kKeepOff ? 128 / kGroup : 1];
+  // int4: -136 times the sums of each group's activations, as the first operand of a 16x16x4 product
+  // with the scales: lane 16 q + c has row c, group 4 i + q
+  float sums[kSums];
   auto load_activations = [&](const RowBlock& b) {
     int r = min(b.lo + col, b.hi - 1);   // surplus rows repeat the last
     if (p.a_rows) r = min(max(p.a_rows[r] / p.a_div, 0), p.A_rows - 1);
@@ -549,22 +552,27 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
         raw[s][j] = make_uint4(0, 0, 0, 0);
         if (k < K) raw[s][j] = *reinterpret_cast<const uint4*>(ap + k);
       }
-    const uint32_t c136 = 0xc308c308u;
-    const bf16x8 b136 = as_bf16x8(make_uint4(c136, c136, c136, c136));
+    if constexpr (kInt4)
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) sums[i] = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (kInt4) raw[s][j] = order_int4(raw[s][j]);
+        if constexpr (kInt4) {
+          float v[8], t = 0.0f;
+          chunk_to_f32<uint16_t>(raw[s][j], v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t += v[i];
+          const int g = (s * 128 + 32 * j) / kGroup;
+          t = quads_total(t);
+          sums[g / 4] += q == g % 4 ? -136.0f * t : 0.0f;
+          raw[s][j] = order_int4(raw[s][j]);
+        }
         // used here, so that the compiler waits for these loads here and not, with every direct
         // load, in front of each item's products
         asm volatile("" : "+v"(raw[s][j].x), "+v"(raw[s][j].y), "+v"(raw[s][j].z), "+v"(raw[s][j].w));
         a[s][j] = as_bf16x8(raw[s][j]);
-        if constexpr (kKeepOff) {
-          f32x4& o = off[s][32 * j / kGroup];
-          if (32 * j % kGroup == 0) o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][j], b136, o, 0, 0, 0);
-        }
       }
   };
 
@@ -621,52 +629,53 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
     const uint8_t* in = ring + slot * slot_bytes;
     slot = slot + 1 == slots ? 0 : slot + 1;
     // scales
-    uint32_t sc[kWords];
-    {
-      uint32_t shift = 0;   // bytes before the first scale (rows that are not swizzled)
-      if (scale_row % 16 != 0)
-        shift = (uint32_t)((reinterpret_cast<uintptr_t>(p.scales) +
-                            ((size_t)cur.rows.e * p.N + row0_of(cur.tile) + (wseg ? second : 0)) * scale_row) & 15);
-      uint32_t raw[kReads];
-      if constexpr (kInt4) {
+    uint32_t shift = 0;   // bytes before the first scale (rows that are not swizzled)
+    if (scale_row % 16 != 0)
+      shift = (uint32_t)((reinterpret_cast<uintptr_t>(p.scales) +
+                          ((size_t)cur.rows.e * p.N + row0_of(cur.tile) + (wseg ? second : 0)) * scale_row) & 15);
+    uint32_t sc[kInt4 ? 1 : S];   // mxfp4: a step's four bytes
+    if constexpr (!kInt4) {
+      const uint32_t odd = (scale_from[0] + shift) & 3;   // the same for every word
+      uint32_t raw[S + 1];
 #pragma unroll
-        for (int w = 0; w < kReads; ++w)
-          raw[w] = *reinterpret_cast<const uint32_t*>(in + scale_from[w / kFromWords] + shift + 4 * (w % kFromWords));
+      for (int w = 0; w <= S; ++w) raw[w] = *reinterpret_cast<const uint32_t*>(in + ((scale_from[w] + shift) & ~3u));
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) sc[w] = raw[w] & scale_ok[w];   // past K: 0
-      } else {
-        const uint32_t odd = (scale_from[0] + shift) & 3;   // the same for every word
-#pragma unroll
-        for (int w = 0; w < kReads; ++w)
-          raw[w] = *reinterpret_cast<const uint32_t*>(in + ((scale_from[w] + shift) & ~3u));
-#pragma unroll
-        for (int w = 0; w < kWords; ++w)   // past K: 2^0
-          sc[w] = (__builtin_amdgcn_alignbyte(raw[w + 1], raw[w], odd) & scale_ok[w]) | (0x7f7f7f7fu & ~scale_ok[w]);
-      }
+      for (int w = 0; w < S; ++w)   // past K: 2^0
+        sc[w] = (__builtin_amdgcn_alignbyte(raw[w + 1], raw[w], odd) & scale_ok[w]) | (0x7f7f7f7fu & ~scale_ok[w]);
     }
     // two sums, so that a product need not wait for the one before it
     f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+    if constexpr (kInt4) {   // the offsets of all groups
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) {
+        const int g = 4 * i + q;
+        const int from = kGroup > 32 ? sum_from[kGroup > 32 ? i : 0] : scale_from[kGroup > 32 ? 0 : i] + 4 * q;
+        const float f = *reinterpret_cast<const float*>(in + from + shift);
+        const bool there = g < kGroups && wave * S * 128 + g * kGroup < K;
+        acc[i & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(sums[i], there ? f : 0.0f, acc[i & 1], 0, 0, 0);
+      }
+    }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const uint4 v = *reinterpret_cast<const uint4*>(in + code_from[s]);
       uint32_t c[4] = {v.x, v.y, v.z, v.w};
       transpose4(c);
       if constexpr (kInt4) {
-        uint32_t c136 = 0xc308c308u;
-        if constexpr (!kKeepOff) asm volatile("" : "+v"(c136));   // or the compiler keeps them after all
-        const bf16x8 b136 = as_bf16x8(make_uint4(c136, c136, c136, c136));
+        float f[128 / kGroup];   // past K: 0
+#pragma unroll
+        for (int i = 0; i < 128 / kGroup; ++i) {
+          f[i] = *reinterpret_cast<const float*>(in + scale_from[s] + shift + 4 * i);
+          if ((wave * S + s) * 128 + i * kGroup >= K) f[i] = 0.0f;
+        }
         f32x4 d;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if constexpr (!kKeepOff)
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][j], b136, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-          else if (32 * j % kGroup == 0)
-            d = off[s][32 * j / kGroup];
+          if (32 * j % kGroup == 0) d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
           d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][j], as_bf16x8(unpack_int4(c[j])), d, 0, 0, 0);
           if (32 * (j + 1) % kGroup == 0)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              acc[j & 1][e] = fmaf(__uint_as_float(sc[s * (128 / kGroup) + 32 * j / kGroup]), d[e], acc[j & 1][e]);
+              acc[j & 1][e] = fmaf(f[32 * j / kGroup], d[e], acc[j & 1][e]);
         }
       } else {
 #pragma unroll
@@ -687,43 +696,39 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   finish(prev, n - 1);
 }
 
-// How a launch is cut.  stream: the streaming kernel, 16 rows a block.  Otherwise MT row tiles of 16
-// and NT weight tiles a workgroup.
+// How a launch is cut: the streaming kernel where its waves hold the activations of a whole row,
+// else NT weight tiles a workgroup.
 struct FourbitCut {
   bool stream;
-  int MT, NT;
-  int lds;                // dynamic LDS bytes of a workgroup
+  int NT;
+  long long lds;          // dynamic LDS bytes of a workgroup
   long long workgroups;   // streaming: items
 };
 
 constexpr int kMaxLds = 64 << 10;   // dynamic LDS of a launch
-#ifndef FB_T1
-#define FB_T1 8
-#define FB_T2 24
-#endif
 
-static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, long long K, int step_bytes, bool silu) {
+static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, long long K, bool int4, int group, bool silu) {
   FourbitCut c{};
-  if (M_rows <= (long long)FB_T1 * E && K <= kStreamWaves * kStreamMaxS * 128) {
+  if (K <= kStreamWaves * stream_max_steps(int4, group) * 128) {
     c.stream = true;
-    c.workgroups = fourbit_blocks(M_rows, E, 16) * ((n_out + (silu ? 7 : 15)) / (silu ? 8 : 16));
+    c.workgroups = fourbit_blocks(M_rows, E) * ((n_out + (silu ? 7 : 15)) / (silu ? 8 : 16));
     return c;
   }
-  c.MT = M_rows <= 8ll * E ? 1 : M_rows <= (long long)FB_T2 * E ? 2 : 4;
   const int per = silu ? 2 : 1;   // weight tiles of an output tile
+  const int step_bytes = kStep / group * (int4 ? 4 : 1);
   // the scales of the tiles' rows; afterwards the waves' sums
   const auto lds = [&](int nt) {
-    return std::max<long long>((long long)nt * 16 * scale_row_bytes(K, step_bytes), kFbWaves * nt * c.MT * 1024);
+    return std::max<long long>((long long)nt * 16 * scale_row_bytes(K, step_bytes), kFbWaves * nt * 1024);
   };
-  c.NT = std::max(4 / c.MT, per);
+  c.NT = 4;
   while (c.NT > per && lds(c.NT) > kMaxLds) c.NT /= 2;
-  c.lds = (int)std::min<long long>(lds(c.NT), INT_MAX);
-  c.workgroups = fourbit_blocks(M_rows, E, 16 * c.MT) * ((n_out + 16 * (c.NT / per) - 1) / (16 * (c.NT / per)));
+  c.lds = lds(c.NT);
+  c.workgroups = fourbit_blocks(M_rows, E) * ((n_out + 16 * (c.NT / per) - 1) / (16 * (c.NT / per)));
   return c;
 }
 
 bool fourbit_fits(long long M_rows, int E, long long N, long long K, bool int4, int group, bool silu) {
-  const FourbitCut c = fourbit_cut(M_rows, E, silu ? N / 2 : N, K, kStep / group * (int4 ? 4 : 1), silu);
+  const FourbitCut c = fourbit_cut(M_rows, E, silu ? N / 2 : N, K, int4, group, silu);
   // a grid holds fewer than 2^32 threads; items are counted in 32 bits
   return c.stream ? c.workgroups <= INT_MAX : c.workgroups < (1ll << 24) && c.lds <= kMaxLds;
 }
@@ -737,14 +742,15 @@ static hipError_t launch_fourbit_stream(const FourbitArgs& a, long long items, h
     hipLaunchKernelGGL((fourbit_stream_kernel<kInt4, kGroup, kSilu, S>), dim3(grid), dim3(kStreamWaves * 64), 0, stream, a);
     return hipGetLastError();
   };
-  switch ((steps + kStreamWaves - 1) / kStreamWaves) {
-    case 1: return go(std::integral_constant<int, 1>{});
-    case 2: return go(std::integral_constant<int, 2>{});
-    case 3: return go(std::integral_constant<int, 3>{});
-    case 4: return go(std::integral_constant<int, 4>{});
-    case 5: return go(std::integral_constant<int, 5>{});
-    case 6: return go(std::integral_constant<int, 6>{});
-    case 7: return go(std::integral_constant<int, 7>{});
+  const int S = (steps + kStreamWaves - 1) / kStreamWaves;
+  if (S == 1) return go(std::integral_constant<int, 1>{});
+  if (S == 2) return go(std::integral_constant<int, 2>{});
+  if (S == 3) return go(std::integral_constant<int, 3>{});
+  if (S == 4) return go(std::integral_constant<int, 4>{});
+  if (S == 5) return go(std::integral_constant<int, 5>{});
+  if constexpr (stream_max_steps(kInt4, kGroup) > 5) {
+    if (S == 6) return go(std::integral_constant<int, 6>{});
+    if (S == 7) return go(std::integral_constant<int, 7>{});
   }
   return hipErrorInvalidValue;
 }
@@ -752,23 +758,20 @@ static hipError_t launch_fourbit_stream(const FourbitArgs& a, long long items, h
 template <bool kInt4, int kGroup, bool kSilu>
 static hipError_t launch_fourbit_s(const FourbitLaunch& p, hipStream_t stream) {
   const FourbitCut cut =
-      fourbit_cut(p.M_rows, p.E, kSilu ? p.N / 2 : p.N, p.K, kStepScaleBytes<kInt4, kGroup>, kSilu);
+      fourbit_cut(p.M_rows, p.E, kSilu ? p.N / 2 : p.N, p.K, kInt4, kGroup, kSilu);
   const FourbitArgs a{static_cast<const uint16_t*>(p.A), p.a_rows, p.a_div, (int)p.a_total,
                       static_cast<const uint8_t*>(p.codes), p.scales, p.offsets, p.E, (int)p.M_rows, (int)p.N,
                       (int)p.K, p.C, p.c_f32};
   if (cut.stream) return launch_fourbit_stream<kInt4, kGroup, kSilu>(a, cut.workgroups, stream);
   const dim3 grid((unsigned)cut.workgroups), block(kFbWaves * 64);
-#define MOE_FOURBIT(MT_, NT_)                                                                              \
-  if (cut.MT == MT_ && cut.NT == NT_) {                                                                   \
-    hipLaunchKernelGGL((fourbit_kernel<kInt4, kGroup, kSilu, MT_, NT_>), grid, block, cut.lds, stream, a); \
-    return hipGetLastError();                                                                             \
+#define MOE_FOURBIT(NT_)                                                                                    \
+  if (cut.NT == NT_) {                                                                                      \
+    hipLaunchKernelGGL((fourbit_kernel<kInt4, kGroup, kSilu, NT_>), grid, block, (size_t)cut.lds, stream, a); \
+    return hipGetLastError();                                                                               \
   }
-  if constexpr (!kSilu) { MOE_FOURBIT(1, 1) }
-  MOE_FOURBIT(1, 2)
-  MOE_FOURBIT(1, 4)
-  if constexpr (!kSilu) { MOE_FOURBIT(2, 1) }
-  MOE_FOURBIT(2, 2)
-  MOE_FOURBIT(4, (kSilu ? 2 : 1))
+  if constexpr (!kSilu) { MOE_FOURBIT(1) }
+  MOE_FOURBIT(2)
+  MOE_FOURBIT(4)
 #undef MOE_FOURBIT
   return hipErrorInvalidValue;
 }

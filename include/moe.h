@@ -426,8 +426,8 @@ moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E,
  *                written as exact zeros.
  *
  * Any number of rows is computed; the weights are read once per 16 rows of an
- * expert (64 where the launch has more than 8 rows per expert on average), so
- * with many rows per expert moe_grouped_gemm on bf16 weights is faster.
+ * expert, so with many rows per expert moe_grouped_gemm on bf16 weights is
+ * faster.
  * Accumulation is f32, C is rounded once.  mxfp4 values are taken as bf16
  * (exact while they are normal bf16 numbers); int4 values are not rounded at
  * all.
