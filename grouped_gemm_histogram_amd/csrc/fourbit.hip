@@ -398,7 +398,7 @@ struct StreamCfg {
   // register's reload would wait for the direct loads before it), else one
   static constexpr int kPerCu = 2 * (2 * kSlotKb + kFixedKb) <= 160 && S <= (kInt4 && kGroup == 32 ? 2 : 3) ? 2 : 1;
   static constexpr int kRingKb = 160 / kPerCu - kFixedKb;
-  static constexpr int kMaxSlots = std::min(8, 63 / kLoads + 2);   // vmcnt counts to 63
+  static constexpr int kMaxSlots = std::min(8, 63 / kLoads + 1);   // vmcnt counts to 63
   static_assert(kRingKb >= 2 * kSlotKb, "ring");
 };
 
@@ -426,13 +426,8 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   };
   const RowBlocks rows_of(p.offsets, p.E, p.M_rows);
   // rows without an expert are zero
-  {
-    const int V = rows_of.at(p.E);
-    const long long n = (long long)(p.M_rows - V) * n_out;
-    for (long long i = (long long)blockIdx.x * W * 64 + threadIdx.x; i < n;
-         i += (long long)gridDim.x * W * 64)
-      store(V + (int)(i / n_out), (int)(i % n_out), 0.0f);
-  }
+  for (int r = uniform(rows_of.at(p.E)) + (int)blockIdx.x; r < p.M_rows; r += (int)gridDim.x)
+    for (int c = threadIdx.x; c < n_out; c += W * 64) store(r, c, 0.0f);
   const int items = rows_of.count() * tiles;
   const int share = uniform(items / (int)gridDim.x), extra = items - share * (int)gridDim.x;
   const int first = (int)blockIdx.x * share + min((int)blockIdx.x, extra);
@@ -441,6 +436,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
 
   // ---- this lane's part of the direct loads
   const int pieces = K / 32, row_bytes = K / 2;
+  const float inv_pieces = 1.0f / (float)pieces;
   const int code_kb = (8 * row_bytes + 1023) / 1024;      // a segment's loads
   uint32_t code_at[S];                                     // source, from an item's first row
   int code_to[S];                                          // target, from the slot; < 0: the spare KiB
@@ -448,9 +444,8 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   for (int j = 0; j < S; ++j) {
     const int load = wave * S + j, seg = (load >= code_kb) + (load >= 2 * code_kb);
     const int i = min((load - seg * code_kb) * 64 + lane, 8 * pieces - 1);   // piece of the segment, as it lies in LDS
-    int r = 0;
-#pragma unroll
-    for (int m = 1; m < 8; ++m) r += i >= m * pieces;
+    // i / pieces: i + 1/2 is at least 1 / (2 pieces) from a multiple, far more than f32 rounds off
+    const int r = (int)(((float)i + 0.5f) * inv_pieces);
     const int pos = i - r * pieces;
     const int row = kSilu ? min(r, n_out - 1) : min(seg * 8 + r, n_out - 1);
     code_at[j] = (uint32_t)(row + (kSilu ? seg * n_out : 0)) * (uint32_t)row_bytes +
@@ -460,6 +455,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   }
   const int scale_row = K / kGroup * Cfg::kScaleBytes;     // bytes of scales of a weight row
   const int scale_pieces = scale_row % 16 == 0 ? scale_row / 16 : 1;   // odd rows are not swizzled
+  const float inv_scale_pieces = 1.0f / (float)scale_pieces;
   const int rows0 = min(8, n_out);                         // rows of a segment that exist
   const int second = kSilu ? n_out : n_out > 8 ? 8 : 0;    // first row of the second segment
   const int rows1 = kSilu ? rows0 : max(min(8, n_out - 8), 1);
@@ -472,9 +468,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   for (int j = 0; j < Cfg::kScaleLoads; ++j) {
     const int load = wave * Cfg::kScaleLoads + j, seg = (load >= scale_kb) + (load >= 2 * scale_kb);
     const int i = (load - seg * scale_kb) * 64 + lane;
-    int r = 0;
-#pragma unroll
-    for (int m = 1; m <= 8; ++m) r += i >= m * scale_pieces;
+    const int r = (int)(((float)i + 0.5f) * inv_scale_pieces);
     scale_i[j] = i ^ (scale_row % 16 == 0 && r < 8 ? row_swizzle(scale_pieces, seg * 8 + r) : 0);
   }
 
@@ -590,12 +584,12 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   const int first_block = uniform(first / tiles);
   Cursor load{first_block, uniform(first - first_block * tiles), rows_of.find(first_block)};
   Cursor cur = load, prev = load;
-  for (int i = 0; i < min(n, slots - 1); ++i) {
+  for (int i = 0; i < min(n, slots); ++i) {
     issue(load.rows, load.tile, i);
     next(load);
   }
   load_activations(cur.rows);
-  int slot = 0, next_slot = slots - 1;
+  int slot = 0, free_slot = slots - 1;   // of this item, of the one before
   // sums of an item, each wave's in turn to the front: rows * kRows outputs over the threads
   auto finish = [&](const Cursor& c, int i) {
     const int rows = c.rows.hi - c.rows.lo;
@@ -617,14 +611,14 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   for (int i = 0; i < n; ++i) {
     // loads of this item have landed; LDS is drained: everyone's reads of the previous slot and
     // writes of sums are behind the barrier
-    wait_slices<Cfg::kLoads, Cfg::kMaxSlots - 2, true>(min(slots - 2, n - 1 - i));
+    wait_slices<Cfg::kLoads, Cfg::kMaxSlots - 1, true>(min(slots - (i == 0 ? 1 : 2), n - 1 - i));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (i + slots - 1 < n) {
-      issue(load.rows, load.tile, next_slot);
+    if (i > 0 && i + slots - 1 < n) {
+      issue(load.rows, load.tile, free_slot);
       next(load);
     }
-    next_slot = next_slot + 1 == slots ? 0 : next_slot + 1;
+    free_slot = slot;
     if (i > 0) finish(prev, i - 1);
     const uint8_t* in = ring + slot * slot_bytes;
     slot = slot + 1 == slots ? 0 : slot + 1;
