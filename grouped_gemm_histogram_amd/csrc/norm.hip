@@ -27,7 +27,7 @@ __global__ __launch_bounds__(kNormWaves<W> * 64) void norm_kernel(
   constexpr int EL = kRowEl<T>;
   constexpr int kWaves = kNormWaves<W>;
   constexpr int kSlots = kWaves / W;   // rows at a time
-  __shared__ float red[2 * 2 * kWaves];
+  __shared__ float red[2 * kMaxSums * kWaves];
   const int wave = threadIdx.x >> 6;
   const int slot = wave / W;
   const int rl = (wave % W) * kWave + lane_id();   // lane within the row

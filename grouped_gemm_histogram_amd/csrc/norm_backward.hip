@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kNbWaves<W> * 64) void norm_backward_kernel(
   constexpr int EL = kRowEl<T>;
   constexpr int kWaves = kNbWaves<W>;
   constexpr int kSlots = kWaves / W;
-  __shared__ float red[2 * 2 * kWaves];
+  __shared__ float red[2 * kMaxSums * kWaves];
   __shared__ float merge[kSlots > 1 ? kSlots / 2 * W * kWave : 1][kSlots > 1 ? C * EL + 1 : 1];   // a row a thread, odd
   const int wave = threadIdx.x >> 6;
   const int slot = wave / W;

@@ -123,16 +123,19 @@ __device__ __forceinline__ float wave_total(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-// Sums of N values over the W waves of a row; every lane gets them.  red: 2 * N floats of LDS per
-// wave of the block; `buf` (0 or 1) alternates between consecutive calls, so that the barrier of
-// the call in between separates a buffer's readers from its next writers.
+// Sums of N values over the W waves of a row; every lane gets them.  red: two buffers of kMaxSums
+// floats per wave of the block; `buf` (0 or 1) alternates between consecutive calls, so that the
+// barrier of the call in between separates a buffer's readers from its next writers, whatever N
+// each call has.
+constexpr int kMaxSums = 2;
 template <int W, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int buf, int nwaves) {
+  static_assert(N <= kMaxSums, "a buffer's floats per wave");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_total(v[i]);
   if constexpr (W > 1) {
     const int wave = threadIdx.x >> 6;
-    float* mine = red + buf * nwaves * N;
+    float* mine = red + buf * nwaves * kMaxSums;
     if (lane_id() == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) mine[wave * N + i] = v[i];

@@ -82,6 +82,18 @@ def test_layer_norm_far_from_zero_constant_and_special_rows():
     assert (z == 0).all()
 
 
+@pytest.mark.parametrize("H", [2880, 7168, 20001])
+def test_layer_norm_same_rows_same_bits(H):
+    """Many rows over several waves each: a row's result depends on the row alone."""
+    import grouped_gemm_histogram_amd as g
+    x = rand(9, 1, H, dtype=torch.bfloat16, shift=1.0).repeat(12000, 1)
+    say(f"layer_norm same rows H={H}")
+    y, stats = g.layer_norm(x, return_stats=True)
+    assert (y == y[0]).all() and (stats.mean == stats.mean[0]).all() and (stats.rstd == stats.rstd[0]).all()
+    dx = g.layer_norm_backward(y, x, stats).dx
+    assert (dx == dx[0]).all()
+
+
 def test_layer_norm_in_place_no_rows_and_refusals():
     import grouped_gemm_histogram_amd as g
     for H in (2880, 2881):
