@@ -6,19 +6,20 @@
 // 2^(scale - 127), one e8m0 byte per 32 channels.  Codes are [E, N, K/2], the even channel in the
 // low nibble.
 //
-// A workgroup has up to 16 * MT rows of one expert and 16 columns (with SiLU * up: 16 gate and
-// 16 up columns); its waves split K and join their f32 sums in LDS in wave order.  A lane loads
-// 16 bytes of codes, 32 channels of one column, and turns them into bf16 MFMA operands in
-// registers: the sixteen rows of v_mfma_f32_16x16x32_bf16 make the product free at any row
-// count, the weights' bytes bound it.
+// The bytes of the weights of the experts that have rows bound it: they are read once per 16 rows.
+// The sixteen rows of v_mfma_f32_16x16x32_bf16 make the products of 1 to 16 rows cost the same.
+// Two kernels: fourbit_stream_kernel where eight waves can hold the activations of a whole row in
+// registers (K to 7168, int4 groups of 32 to 5120), fourbit_kernel for longer rows.
 //
-// mxfp4: e2m1 * 2^s is exact in bf16, so the scale is applied while unpacking
-// (v_cvt_scalef32_pk_bf16_fp4); the four channel octets of a lane go to four MFMAs.
+// mxfp4: e2m1 * 2^s is exact in bf16 (while normal), so the scale is applied while unpacking
+// (v_cvt_scalef32_pk_bf16_fp4).
 // int4: code * scale is not exact in bf16, so the MFMA runs on 128 + code (the nibble put under
-// bf16's 128) and the scale multiplies its f32 result: the four lane groups first swap 4 x 4
-// words (v_permlane32_swap, v_permlane16_swap) so that an MFMA has 32 consecutive channels, all
-// of one scale.  The offset 136 leaves through a second MFMA with the constant weight -136,
-// shared by gate and up.  Its terms are at most 17 times the true ones, 2^-24 each.
+// bf16's 128) and the scale multiplies its f32 result; MFMAs have 32 consecutive channels, all of
+// one scale, after a 4 x 4 transpose of words between the lane groups (v_permlane32_swap,
+// v_permlane16_swap).  The offset leaves as -136 * sum_g scale_g * (sum of the group's
+// activations): in the streaming kernel one 16x16x4 f32 product per four groups of sums that are
+// kept with the activations, in the other a second MFMA with the constant weight -136.  Its terms
+// are at most 17 times the true ones, 2^-24 each.
 
 #include <limits.h>
 
@@ -79,13 +80,21 @@ __device__ __forceinline__ uint4 unpack_mxfp4(uint32_t v, uint32_t e8m0) {
 }
 
 // The row blocks of a launch: every expert's rows in blocks of 16, expert by expert.  Each lane keeps
-// the running count of its consecutive experts' blocks; all 64 lanes take part in each call.
+// the running count of its consecutive experts' blocks; all 64 lanes take part in each call.  Offsets
+// that do not ascend give blocks of some rows in [0, M_rows), and no more of them than the host allows
+// for (most_blocks).
 struct RowBlock {
   int e, lo, hi;   // rows [lo, hi) of expert e
 };
 
 // a value that is the same in all lanes, into a scalar register (quotients are computed in vector ones)
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// at most one partial block per expert that has rows, and one of rows without an expert
+__host__ __device__ constexpr long long most_blocks(long long M_rows, int E) {
+  const long long n = M_rows / 16 + (E < M_rows ? E : M_rows) + 1;
+  return M_rows < n ? M_rows : n;
+}
 
 struct RowBlocks {
   const int* offsets;
@@ -94,7 +103,7 @@ struct RowBlocks {
   int lo0, hi0, mine, incl;
 
   __device__ __forceinline__ int at(int e) const { return min(max(offsets[min(e, E)], 0), M_rows); }
-  __device__ __forceinline__ int blocks(int lo, int hi) const { return max(hi - lo + BM - 1, 0) / BM; }
+  __device__ __forceinline__ int blocks(int lo, int hi) const { return hi > lo ? (hi - lo - 1) / BM + 1 : 0; }
 
   __device__ __forceinline__ RowBlocks(const int* offsets_, int E_, int M_rows_)
       : offsets(offsets_), E(E_), M_rows(M_rows_), per((E_ + kWave - 1) / kWave) {
@@ -115,7 +124,9 @@ struct RowBlocks {
     }
   }
 
-  __device__ __forceinline__ int count() const { return __builtin_amdgcn_readlane(incl, 63); }
+  __device__ __forceinline__ int count() const {
+    return min(max(__builtin_amdgcn_readlane(incl, 63), 0), (int)most_blocks(M_rows, E));
+  }
 
   __device__ __forceinline__ RowBlock find(int block) const {   // 0 <= block < count()
     const int owner = __builtin_ctzll(__ballot(incl > block) | (1ull << 63));
@@ -127,7 +138,8 @@ struct RowBlocks {
       lo = hi;
       hi = uniform(at(owner * per + i + 2));
     }
-    return {uniform(owner * per + i), uniform(lo + rest * BM), uniform(min(lo + (rest + 1) * BM, hi))};
+    lo += min(max(rest, 0), max(blocks(lo, hi) - 1, 0)) * BM;
+    return {uniform(min(owner * per + i, E - 1)), uniform(lo), uniform(lo + min(hi - lo, BM))};
   }
 };
 
@@ -187,7 +199,11 @@ __device__ __forceinline__ void stage_scales(const uint8_t* __restrict__ scales,
 }
 
 // Long weight rows: blocks of 16 rows of an expert, NT weight tiles of 16 rows (with SiLU * up the even
-// ones are gate and the odd ones up).  kGroup: channels per scale (mxfp4: 32).
+// ones are gate and the odd ones up).  kGroup: channels per scale (mxfp4: 32).  The waves split K and
+// join their f32 sums in LDS in wave order.  A load instruction takes whole 128-byte lines of 8 weight
+// rows, which `halves` and transpose4 bring into the MFMA's order: lane loads of 64 bytes of 16 rows
+// took 349 us where this takes 202 (int4, 128 routes over 256 experts, 7168 x 2048), the streaming
+// kernel 160.
 template <bool kInt4, int kGroup, bool kSilu, int NT>
 __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p) {
   constexpr int BM = 16;
@@ -237,7 +253,7 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
 #pragma unroll
     for (int h = 0; h < 2; ++h) wat[t][h] = wrow(t, (col & 7) + 8 * h) * (uint32_t)(K / 2) + 16 * piece;
   }
-  int arow = min(blk.lo + col, blk.hi - 1);   // surplus rows repeat the last
+  int arow = min(blk.lo + max(min(col, blk.hi - blk.lo - 1), 0), p.M_rows - 1);   // surplus rows repeat the last
   if (p.a_rows) arow = min(max(p.a_rows[arow] / p.a_div, 0), p.A_rows - 1);
   const uint16_t* ap = p.A + (size_t)arow * K;
   f32x4 acc[NT];
@@ -341,12 +357,9 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
   }
 }
 
-// row blocks: at most one partial block per expert that has rows, and one of rows without an expert
-static long long fourbit_blocks(long long M_rows, int E) {
-  return std::min<long long>(M_rows, M_rows / 16 + std::min<long long>(E, M_rows) + 1);
-}
-
 // ---------------------------------------------------------------- few rows per expert: streaming
+//
+// Bound by the weights' bytes from HBM: @@FIG@@
 //
 // A launch is a fixed number of workgroups of eight waves.  Each takes an even share of the items
 // (a block of up to 16 rows of one expert, 16 weight rows; with SiLU * up 8 gate and 8 up rows) in
@@ -355,6 +368,12 @@ static long long fourbit_blocks(long long M_rows, int E) {
 // for it.  Wave w has the activations of S steps of 128 channels in registers for as long as the
 // row block lasts; the waves' f32 sums meet in LDS in wave order.  One barrier an item: behind it
 // the next item's bytes have landed, the previous item's slot is free and its sums are complete.
+//
+// Not kept, being slower: workgroups of four waves, one workgroup per CU where two fit, items dealt
+// to the workgroups in turn (174-265 us for 160).  More than 16 rows per
+// expert: 32- and 64-row blocks in the other kernel, which read the weights fewer times, took 107 / 192
+// / 314 and 169 / 212 / 351 us at 16 / 32 / 64 rows per expert where this takes 80 / 128 / 211 (mxfp4,
+// 32 experts, 5760 x 2880).
 //
 // A weight row's 16-byte pieces lie in its LDS row in the order piece ^ swizzle, chosen so that the
 // 16 lanes that read one piece of 16 rows hit different banks.
@@ -426,8 +445,8 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   };
   const RowBlocks rows_of(p.offsets, p.E, p.M_rows);
   // rows without an expert are zero
-  for (int r = uniform(rows_of.at(p.E)) + (int)blockIdx.x; r < p.M_rows; r += (int)gridDim.x)
-    for (int c = threadIdx.x; c < n_out; c += W * 64) store(r, c, 0.0f);
+  for (long long r = (long long)rows_of.at(p.E) + blockIdx.x; r < p.M_rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < n_out; c += W * 64) store((int)r, c, 0.0f);
   const int items = rows_of.count() * tiles;
   const int share = uniform(items / (int)gridDim.x), extra = items - share * (int)gridDim.x;
   const int first = (int)blockIdx.x * share + min((int)blockIdx.x, extra);
@@ -534,7 +553,8 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   // with the scales: lane 16 q + c has row c, group 4 i + q
   float sums[kSums];
   auto load_activations = [&](const RowBlock& b) {
-    int r = min(b.lo + col, b.hi - 1);   // surplus rows repeat the last
+    int r = b.lo + max(min(col, b.hi - b.lo - 1), 0);   // surplus rows repeat the last
+    r = min(r, p.M_rows - 1);
     if (p.a_rows) r = min(max(p.a_rows[r] / p.a_div, 0), p.A_rows - 1);
     const uint16_t* ap = p.A + (size_t)r * K + 8 * q;
     uint4 raw[S][4];
@@ -705,7 +725,7 @@ static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, long lon
   FourbitCut c{};
   if (K <= kStreamWaves * stream_max_steps(int4, group) * 128) {
     c.stream = true;
-    c.workgroups = fourbit_blocks(M_rows, E) * ((n_out + (silu ? 7 : 15)) / (silu ? 8 : 16));
+    c.workgroups = most_blocks(M_rows, E) * ((n_out + (silu ? 7 : 15)) / (silu ? 8 : 16));
     return c;
   }
   const int per = silu ? 2 : 1;   // weight tiles of an output tile
@@ -717,7 +737,7 @@ static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, long lon
   c.NT = 4;
   while (c.NT > per && lds(c.NT) > kMaxLds) c.NT /= 2;
   c.lds = lds(c.NT);
-  c.workgroups = fourbit_blocks(M_rows, E) * ((n_out + 16 * (c.NT / per) - 1) / (16 * (c.NT / per)));
+  c.workgroups = most_blocks(M_rows, E) * ((n_out + 16 * (c.NT / per) - 1) / (16 * (c.NT / per)));
   return c;
 }
 

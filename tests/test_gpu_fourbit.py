@@ -219,6 +219,36 @@ def test_matvec_same_row_many_times_and_bad_maps():
     np.testing.assert_array_equal(host(out), want)
 
 
+def test_offsets_that_do_not_ascend():
+    """Such offsets are a mistake, but only rows of the output are written."""
+    import grouped_gemm_histogram_amd as g
+    codes, scales = weights(3, 32, 64, "int4", 32, 1, exact=True)
+    a = torch.randint(-2, 3, (48, 64), generator=gen(2)).to(torch.bfloat16)
+    buf = torch.full((48 + 64, 32), 7.0, device=DEV)
+    say("offsets 0 40 8 48")
+    out = g.grouped_matvec_fourbit(a.to(DEV), codes.to(DEV), scales.to(DEV),
+                                   torch.tensor([0, 40, 8, 48], dtype=torch.int32, device=DEV), out=buf[32:80])
+    first, _ = reference(host(a), codes, scales, np.array([0, 48, 48, 48]), False)
+    last, _ = reference(host(a), codes, scales, np.array([0, 0, 0, 48]), False)
+    np.testing.assert_array_equal(host(out)[:8], first[:8])
+    np.testing.assert_array_equal(host(out)[40:], last[40:])
+    assert (buf[:32] == 7).all() and (buf[80:] == 7).all()
+
+
+def test_mxfp4_smallest_scales():
+    """Scale bytes 0 and 1, on codes whose values 2^-126 and up are normal bf16 numbers."""
+    import grouped_gemm_histogram_amd as g
+    row = torch.tensor([4 | 5 << 4, 6 | 7 << 4, 12 | 13 << 4, 14 | 15 << 4], dtype=torch.uint8).repeat(4)   # 2 3 4 6 and negatives
+    c = row.view(1, 1, 16).repeat(1, 2, 1)
+    s = torch.tensor([0, 1], dtype=torch.uint8).view(1, 2, 1)
+    a = torch.zeros(8, 32)
+    a[torch.arange(8), torch.arange(8)] = 2.0 ** 100
+    out = g.grouped_matvec_fourbit(a.to(torch.bfloat16).to(DEV), c.to(DEV), s.to(DEV),
+                                   torch.tensor([0, 8], dtype=torch.int32, device=DEV), out_dtype=torch.float32)
+    want = ofb.dequantize(c[0].numpy(), s[0].numpy())[:, :8].T * 2.0 ** 100
+    np.testing.assert_array_equal(host(out), want)
+
+
 def test_mxfp4_scale_range():
     """Every scale byte at which all values are normal bf16 numbers, and the byte that means NaN."""
     import grouped_gemm_histogram_amd as g
