@@ -8,6 +8,10 @@
 // loads in flight meanwhile), writes dx, and adds each row to f32 sums of its columns that stay in
 // registers until the block's last row.  The sums go to the workspace, one row per row slot, and
 // a second kernel adds those rows in a fixed order: no atomics, so results do not vary.
+//
+// Bound by HBM: x and dy read, dx written.  bf16 8192 x 7168 takes 71 us (5.0 TB/s) and 4.7 for the
+// sums of the partial rows; 4096 x 2880 20.2 and 4.0, where its 71 MB alone would take 12 to 14: with
+// 16 rows a block, filling and draining the pipeline and the columns' sums show.
 
 #include <algorithm>
 
@@ -16,7 +20,7 @@
 
 namespace moe {
 
-// waves of a block
+// waves of a block: with 16 in every block the columns' sums spill (126 us for 71 at 8192 x 7168)
 template <int W>
 constexpr int kNbWaves = W < 8 ? 8 : W;
 
@@ -168,7 +172,8 @@ __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float* __rest
   }
 }
 
-// blocks of a launch, each with one row of partial sums
+// blocks of a launch, each with one row of partial sums; 512 take 81 us for 71 at 8192 x 7168 and 24.6
+// for 20.2 at 4096 x 2880
 constexpr int kPartRows = 256;
 
 template <typename T, bool kVec>
