@@ -81,20 +81,13 @@ __device__ __forceinline__ uint4 unpack_mxfp4(uint32_t v, uint32_t e8m0) {
 
 // The row blocks of a launch: every expert's rows in blocks of 16, expert by expert.  Each lane keeps
 // the running count of its consecutive experts' blocks; all 64 lanes take part in each call.  Offsets
-// that do not ascend give blocks of some rows in [0, M_rows), and no more of them than the host allows
-// for (most_blocks).
+// that do not ascend have no blocks: the counts and rows below hold only where they do.
 struct RowBlock {
   int e, lo, hi;   // rows [lo, hi) of expert e
 };
 
 // a value that is the same in all lanes, into a scalar register (quotients are computed in vector ones)
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// at most one partial block per expert that has rows, and one of rows without an expert
-__host__ __device__ constexpr long long most_blocks(long long M_rows, int E) {
-  const long long n = M_rows / 16 + (E < M_rows ? E : M_rows) + 1;
-  return M_rows < n ? M_rows : n;
-}
 
 struct RowBlocks {
   const int* offsets;
@@ -103,19 +96,22 @@ struct RowBlocks {
   int lo0, hi0, mine, incl;
 
   __device__ __forceinline__ int at(int e) const { return min(max(offsets[min(e, E)], 0), M_rows); }
-  __device__ __forceinline__ int blocks(int lo, int hi) const { return hi > lo ? (hi - lo - 1) / BM + 1 : 0; }
+  __device__ __forceinline__ int blocks(int lo, int hi) const { return max(hi - lo + BM - 1, 0) / BM; }
 
   __device__ __forceinline__ RowBlocks(const int* offsets_, int E_, int M_rows_)
       : offsets(offsets_), E(E_), M_rows(M_rows_), per((E_ + kWave - 1) / kWave) {
     const int lane = lane_id();
     lo0 = at(lane * per);
     mine = 0;
+    bool ascend = true;
     for (int i = 0, lo = lo0; i < per; ++i) {
       const int hi = at(lane * per + i + 1);
+      ascend &= lo <= hi;
       mine += blocks(lo, hi);
       lo = hi;
       if (i == 0) hi0 = hi;
     }
+    if (__ballot(ascend) != ~0ull) mine = 0;
     incl = mine;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
@@ -124,9 +120,7 @@ struct RowBlocks {
     }
   }
 
-  __device__ __forceinline__ int count() const {
-    return min(max(__builtin_amdgcn_readlane(incl, 63), 0), (int)most_blocks(M_rows, E));
-  }
+  __device__ __forceinline__ int count() const { return __builtin_amdgcn_readlane(incl, 63); }
 
   __device__ __forceinline__ RowBlock find(int block) const {   // 0 <= block < count()
     const int owner = __builtin_ctzll(__ballot(incl > block) | (1ull << 63));
@@ -138,8 +132,7 @@ struct RowBlocks {
       lo = hi;
       hi = uniform(at(owner * per + i + 2));
     }
-    lo += min(max(rest, 0), max(blocks(lo, hi) - 1, 0)) * BM;
-    return {uniform(min(owner * per + i, E - 1)), uniform(lo), uniform(lo + min(hi - lo, BM))};
+    return {uniform(owner * per + i), uniform(lo + rest * BM), uniform(min(lo + (rest + 1) * BM, hi))};
   }
 };
 
@@ -253,7 +246,7 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
 #pragma unroll
     for (int h = 0; h < 2; ++h) wat[t][h] = wrow(t, (col & 7) + 8 * h) * (uint32_t)(K / 2) + 16 * piece;
   }
-  int arow = min(blk.lo + max(min(col, blk.hi - blk.lo - 1), 0), p.M_rows - 1);   // surplus rows repeat the last
+  int arow = min(blk.lo + col, blk.hi - 1);   // surplus rows repeat the last
   if (p.a_rows) arow = min(max(p.a_rows[arow] / p.a_div, 0), p.A_rows - 1);
   const uint16_t* ap = p.A + (size_t)arow * K;
   f32x4 acc[NT];
@@ -357,9 +350,18 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
   }
 }
 
-// ---------------------------------------------------------------- few rows per expert: streaming
+// row blocks: at most one partial block per expert that has rows, and one of rows without an expert
+static long long fourbit_blocks(long long M_rows, int E) {
+  return std::min<long long>(M_rows, M_rows / 16 + std::min<long long>(E, M_rows) + 1);
+}
+
+// ---------------------------------------------------------------- rows of up to 7168 channels: streaming
 //
-// Bound by the weights' bytes from HBM: @@FIG@@
+// Bound by the weights' bytes from HBM: int4 groups of 128, 128 routes over 256 experts of 7168 x 2048
+// take 168 us (789 MB, 4.7 TB/s); int4 groups of 32, 512 routes over 128 of 1536 x 2048, SiLU * up, 59
+// (240 MB, 4.1); mxfp4, 64 routes over 8 of 28672 x 4096 102 (501 MB, 4.9).  One token on four experts
+// of 5760 x 2880, mxfp4 (34 MB) is a chain: 1.8 us launch, 1.2 the experts' scan, 3.4 to the first
+// item's arrival, then 1.7 to 2 us for each of two or three items: 13 us.
 //
 // A launch is a fixed number of workgroups of eight waves.  Each takes an even share of the items
 // (a block of up to 16 rows of one expert, 16 weight rows; with SiLU * up 8 gate and 8 up rows) in
@@ -370,10 +372,10 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
 // the next item's bytes have landed, the previous item's slot is free and its sums are complete.
 //
 // Not kept, being slower: workgroups of four waves, one workgroup per CU where two fit, items dealt
-// to the workgroups in turn (174-265 us for 160).  More than 16 rows per
-// expert: 32- and 64-row blocks in the other kernel, which read the weights fewer times, took 107 / 192
-// / 314 and 169 / 212 / 351 us at 16 / 32 / 64 rows per expert where this takes 80 / 128 / 211 (mxfp4,
-// 32 experts, 5760 x 2880).
+// to the workgroups in turn (174-265 us for 160), all slots filled before the first item instead of all
+// but one (one token 14.1 us for 13.1).  More than 16 rows per expert: 32- and 64-row blocks in the
+// other kernel, which read the weights fewer times, took 107 / 192 / 314 and 169 / 212 / 351 us at
+// 16 / 32 / 64 rows per expert where this takes 80 / 128 / 211 (mxfp4, 32 experts, 5760 x 2880).
 //
 // A weight row's 16-byte pieces lie in its LDS row in the order piece ^ swizzle, chosen so that the
 // 16 lanes that read one piece of 16 rows hit different banks.
@@ -417,7 +419,7 @@ struct StreamCfg {
   // register's reload would wait for the direct loads before it), else one
   static constexpr int kPerCu = 2 * (2 * kSlotKb + kFixedKb) <= 160 && S <= (kInt4 && kGroup == 32 ? 2 : 3) ? 2 : 1;
   static constexpr int kRingKb = 160 / kPerCu - kFixedKb;
-  static constexpr int kMaxSlots = std::min(8, 63 / kLoads + 1);   // vmcnt counts to 63
+  static constexpr int kMaxSlots = std::min(8, 63 / kLoads + 2);   // vmcnt counts to 63
   static_assert(kRingKb >= 2 * kSlotKb, "ring");
 };
 
@@ -445,8 +447,13 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   };
   const RowBlocks rows_of(p.offsets, p.E, p.M_rows);
   // rows without an expert are zero
-  for (long long r = (long long)rows_of.at(p.E) + blockIdx.x; r < p.M_rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < n_out; c += W * 64) store((int)r, c, 0.0f);
+  {
+    const int V = rows_of.at(p.E);
+    const long long n = (long long)(p.M_rows - V) * n_out;
+    for (long long i = (long long)blockIdx.x * W * 64 + threadIdx.x; i < n;
+         i += (long long)gridDim.x * W * 64)
+      store(V + (int)(i / n_out), (int)(i % n_out), 0.0f);
+  }
   const int items = rows_of.count() * tiles;
   const int share = uniform(items / (int)gridDim.x), extra = items - share * (int)gridDim.x;
   const int first = (int)blockIdx.x * share + min((int)blockIdx.x, extra);
@@ -455,7 +462,6 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
 
   // ---- this lane's part of the direct loads
   const int pieces = K / 32, row_bytes = K / 2;
-  const float inv_pieces = 1.0f / (float)pieces;
   const int code_kb = (8 * row_bytes + 1023) / 1024;      // a segment's loads
   uint32_t code_at[S];                                     // source, from an item's first row
   int code_to[S];                                          // target, from the slot; < 0: the spare KiB
@@ -463,8 +469,9 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   for (int j = 0; j < S; ++j) {
     const int load = wave * S + j, seg = (load >= code_kb) + (load >= 2 * code_kb);
     const int i = min((load - seg * code_kb) * 64 + lane, 8 * pieces - 1);   // piece of the segment, as it lies in LDS
-    // i / pieces: i + 1/2 is at least 1 / (2 pieces) from a multiple, far more than f32 rounds off
-    const int r = (int)(((float)i + 0.5f) * inv_pieces);
+    int r = 0;
+#pragma unroll
+    for (int m = 1; m < 8; ++m) r += i >= m * pieces;
     const int pos = i - r * pieces;
     const int row = kSilu ? min(r, n_out - 1) : min(seg * 8 + r, n_out - 1);
     code_at[j] = (uint32_t)(row + (kSilu ? seg * n_out : 0)) * (uint32_t)row_bytes +
@@ -474,7 +481,6 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   }
   const int scale_row = K / kGroup * Cfg::kScaleBytes;     // bytes of scales of a weight row
   const int scale_pieces = scale_row % 16 == 0 ? scale_row / 16 : 1;   // odd rows are not swizzled
-  const float inv_scale_pieces = 1.0f / (float)scale_pieces;
   const int rows0 = min(8, n_out);                         // rows of a segment that exist
   const int second = kSilu ? n_out : n_out > 8 ? 8 : 0;    // first row of the second segment
   const int rows1 = kSilu ? rows0 : max(min(8, n_out - 8), 1);
@@ -487,7 +493,9 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   for (int j = 0; j < Cfg::kScaleLoads; ++j) {
     const int load = wave * Cfg::kScaleLoads + j, seg = (load >= scale_kb) + (load >= 2 * scale_kb);
     const int i = (load - seg * scale_kb) * 64 + lane;
-    const int r = (int)(((float)i + 0.5f) * inv_scale_pieces);
+    int r = 0;
+#pragma unroll
+    for (int m = 1; m <= 8; ++m) r += i >= m * scale_pieces;
     scale_i[j] = i ^ (scale_row % 16 == 0 && r < 8 ? row_swizzle(scale_pieces, seg * 8 + r) : 0);
   }
 
@@ -553,8 +561,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   // with the scales: lane 16 q + c has row c, group 4 i + q
   float sums[kSums];
   auto load_activations = [&](const RowBlock& b) {
-    int r = b.lo + max(min(col, b.hi - b.lo - 1), 0);   // surplus rows repeat the last
-    r = min(r, p.M_rows - 1);
+    int r = min(b.lo + col, b.hi - 1);   // surplus rows repeat the last
     if (p.a_rows) r = min(max(p.a_rows[r] / p.a_div, 0), p.A_rows - 1);
     const uint16_t* ap = p.A + (size_t)r * K + 8 * q;
     uint4 raw[S][4];
@@ -604,12 +611,12 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   const int first_block = uniform(first / tiles);
   Cursor load{first_block, uniform(first - first_block * tiles), rows_of.find(first_block)};
   Cursor cur = load, prev = load;
-  for (int i = 0; i < min(n, slots); ++i) {
+  for (int i = 0; i < min(n, slots - 1); ++i) {
     issue(load.rows, load.tile, i);
     next(load);
   }
   load_activations(cur.rows);
-  int slot = 0, free_slot = slots - 1;   // of this item, of the one before
+  int slot = 0, next_slot = slots - 1;
   // sums of an item, each wave's in turn to the front: rows * kRows outputs over the threads
   auto finish = [&](const Cursor& c, int i) {
     const int rows = c.rows.hi - c.rows.lo;
@@ -631,14 +638,14 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
   for (int i = 0; i < n; ++i) {
     // loads of this item have landed; LDS is drained: everyone's reads of the previous slot and
     // writes of sums are behind the barrier
-    wait_slices<Cfg::kLoads, Cfg::kMaxSlots - 1, true>(min(slots - (i == 0 ? 1 : 2), n - 1 - i));
+    wait_slices<Cfg::kLoads, Cfg::kMaxSlots - 2, true>(min(slots - 2, n - 1 - i));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (i > 0 && i + slots - 1 < n) {
-      issue(load.rows, load.tile, free_slot);
+    if (i + slots - 1 < n) {
+      issue(load.rows, load.tile, next_slot);
       next(load);
     }
-    free_slot = slot;
+    next_slot = next_slot + 1 == slots ? 0 : next_slot + 1;
     if (i > 0) finish(prev, i - 1);
     const uint8_t* in = ring + slot * slot_bytes;
     slot = slot + 1 == slots ? 0 : slot + 1;
@@ -725,7 +732,7 @@ static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, long lon
   FourbitCut c{};
   if (K <= kStreamWaves * stream_max_steps(int4, group) * 128) {
     c.stream = true;
-    c.workgroups = most_blocks(M_rows, E) * ((n_out + (silu ? 7 : 15)) / (silu ? 8 : 16));
+    c.workgroups = fourbit_blocks(M_rows, E) * ((n_out + (silu ? 7 : 15)) / (silu ? 8 : 16));
     return c;
   }
   const int per = silu ? 2 : 1;   // weight tiles of an output tile
@@ -737,11 +744,12 @@ static FourbitCut fourbit_cut(long long M_rows, int E, long long n_out, long lon
   c.NT = 4;
   while (c.NT > per && lds(c.NT) > kMaxLds) c.NT /= 2;
   c.lds = lds(c.NT);
-  c.workgroups = most_blocks(M_rows, E) * ((n_out + 16 * (c.NT / per) - 1) / (16 * (c.NT / per)));
+  c.workgroups = fourbit_blocks(M_rows, E) * ((n_out + 16 * (c.NT / per) - 1) / (16 * (c.NT / per)));
   return c;
 }
 
 bool fourbit_fits(long long M_rows, int E, long long N, long long K, bool int4, int group, bool silu) {
+  if (M_rows > INT_MAX - 64) return false;   // the kernels count up to a block past the rows in 32 bits
   const FourbitCut c = fourbit_cut(M_rows, E, silu ? N / 2 : N, K, int4, group, silu);
   // a grid holds fewer than 2^32 threads; items are counted in 32 bits
   return c.stream ? c.workgroups <= INT_MAX : c.workgroups < (1ll << 24) && c.lds <= kMaxLds;

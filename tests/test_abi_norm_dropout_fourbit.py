@@ -103,6 +103,7 @@ def test_fourbit_refusals(lib):
         assert matvec(lib, **{name: None}) == INVALID, name
     assert matvec(lib, a=ODD) == INVALID and matvec(lib, codes=ODD) == INVALID
     assert matvec(lib, M=1 << 30, rows=1 << 30, N=1 << 20) == UNSUP
+    assert matvec(lib, M=(1 << 31) - 1, rows=(1 << 31) - 1) == UNSUP
 
     q = lambda wd=BF16, E=2, N=4, K=64, fmt=INT4, group=32, w=FAKE: lib.quantize_fourbit(
         w, wd, E, N, K, fmt, group, FAKE, FAKE, None)
