@@ -419,7 +419,9 @@ moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E,
  *                under 2 GiB.  K up to 16128 for int4 groups of 32, 32512 for groups
  *                of 64, 65280 otherwise; beyond, MOE_ERR_UNSUPPORTED where a
  *                workgroup's scales do not fit in LDS.
- *   offsets      device int32 [E+1], read on the device.
+ *                M_rows up to 2^31 - 65.
+ *   offsets      device int32 [E+1], read on the device.  Offsets that do not
+ *                ascend are a mistake: no expert has rows then.
  *   epi          as for moe_grouped_gemm (SiLU*up: N even, N_out = N/2).
  *   C            [M_rows, N_out] of c_dtype (MOE_F32 or MOE_BF16), no
  *                alignment of its rows needed; rows from offsets[E] on are
