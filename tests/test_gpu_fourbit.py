@@ -219,6 +219,39 @@ def test_matvec_same_row_many_times_and_bad_maps():
     np.testing.assert_array_equal(host(out), want)
 
 
+@pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("int4", 128)])
+def test_matvec_arrays_past_32_bits(fmt, group):
+    """The last expert of weights past 4 GiB, and the last rows of an output past 4 GiB."""
+    import grouped_gemm_histogram_amd as g
+    E, N, K = 72, 65536, 2048                          # 64 MiB of codes an expert
+    say(f"matvec past 32 bits: weights {fmt}")
+    gd = torch.Generator(device=DEV).manual_seed(1)
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=gd, device=DEV, dtype=torch.uint8)
+    if fmt == "mxfp4":
+        scales = torch.randint(120, 125, (E, N, K // 32), generator=gd, device=DEV, dtype=torch.uint8)
+    else:
+        scales = torch.rand(E, N, K // group, generator=gd, device=DEV)
+    a = torch.randn(9, K, generator=gen(2)).to(torch.bfloat16).to(DEV)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[E] = 9
+    one = torch.tensor([0, 9], dtype=torch.int32, device=DEV)
+    for epi in ("none", "silu_mul"):
+        out = g.grouped_matvec_fourbit(a, codes, scales, off, epi, out_dtype=torch.float32)
+        want = g.grouped_matvec_fourbit(a, codes[-1:].clone(), scales[-1:].clone(), one, epi, out_dtype=torch.float32)
+        assert torch.equal(out, want) and out.abs().sum() > 0
+    say("matvec past 32 bits: output")
+    M = 40000                                          # x 65536 bf16 columns
+    codes, scales = codes[:1, :, :64].contiguous(), scales[:1, :, :128 // group].contiguous()
+    a = torch.randn(M, 128, generator=gen(3)).to(torch.bfloat16).to(DEV)
+    off = torch.tensor([0, M - 8], dtype=torch.int32, device=DEV)
+    out = g.grouped_matvec_fourbit(a, codes, scales, off)
+    for lo in (0, M - 40):                             # whole blocks of 16 rows, then a part of one
+        hi = min(lo + 48, M - 8)
+        want = g.grouped_matvec_fourbit(a[lo:hi], codes, scales, torch.tensor([0, hi - lo], dtype=torch.int32, device=DEV))
+        assert torch.equal(out[lo:hi], want)
+    assert (out[M - 8:] == 0).all()
+
+
 def test_offsets_that_do_not_ascend():
     """Such offsets are a mistake: no expert has rows then, and nothing past the output is written."""
     import grouped_gemm_histogram_amd as g

@@ -263,7 +263,7 @@ def test_dropout_special_values_in_place_and_refusals():
     with pytest.raises(ValueError, match="residual"):
         g.dropout_add(x, rng_tensor(9), 0.5, residual=r[:5])
     with pytest.raises(RuntimeError, match="overlaps"):
-        g.dropout_add(x[:2048], rng_tensor(9), 0.5, out=x[1024:3072])
+        g.dropout_add(x[:2000], rng_tensor(9), 0.5, out=x[1024:3024])
     with pytest.raises(RuntimeError, match="aligned"):
         g.dropout_add(x[1:9], rng_tensor(9), 0.5)
 
@@ -315,3 +315,38 @@ def test_on_another_stream_and_two_at_once():
         for a, b in zip(got, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1].dx, b[1].dx) and torch.equal(a[2], b[2])
             assert torch.equal(a[1].dweight, b[1].dweight)
+
+
+def test_arrays_past_32_bits():
+    """Element and byte offsets past 2^31 and 2^32: the last rows as in a call on them alone."""
+    import grouped_gemm_histogram_amd as g
+    T, H, n = 140000, 32768, 600                       # 4.59e9 elements, bf16
+    say("layer_norm past 32 bits")
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    x[:n], x[-n:] = rand(1, n, H, dtype=torch.bfloat16), rand(2, n, H, dtype=torch.bfloat16)
+    y, stats = g.layer_norm(x, return_stats=True)
+    for rows in (slice(0, n), slice(T - n, T)):
+        want, ws = g.layer_norm(x[rows], return_stats=True)
+        assert torch.equal(y[rows], want) and torch.equal(stats.rstd[rows], ws.rstd)
+    assert (y[n:-n:1000] == 0).all()
+    say("layer_norm_backward past 32 bits")
+    dx = g.layer_norm_backward(y, x, stats, dx=y).dx    # dy = y
+    for rows in (slice(0, n), slice(T - n, T)):
+        dy, s = g.layer_norm(x[rows], return_stats=True)
+        assert torch.equal(dx[rows], g.layer_norm_backward(dy, x[rows], s).dx)
+    del dx, y
+    say("dropout_add past 32 bits")
+    out = g.dropout_add(x, rng_tensor(3, 7), 0.4)
+    start = (T - n) * H
+    assert torch.equal(out[-n:], g.dropout_add(x[-n:], rng_tensor(3, 7 + start // 8), 0.4))
+    assert torch.equal(out[:n], g.dropout_add(x[:n], rng_tensor(3, 7), 0.4))
+    del out
+    say("unpermute_combine_dropout past 32 bits")
+    k = 2
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    w = torch.full((T // k, k), 0.5, device=DEV)
+    off = torch.tensor([0, T, T], dtype=torch.int32, device=DEV)
+    out = g.unpermute_combine_dropout(x, pos, w, off, k, rng_tensor(3, 7), 0.4)
+    at = (T // k - n // k) * H
+    want = g.unpermute_combine_dropout(x[-n:], pos[:n], w[:n // k], off.clamp(max=n), k, rng_tensor(3, 7 + at // 8), 0.4)
+    assert torch.equal(out[-n // k:], want)
