@@ -8,7 +8,7 @@
 // rows grid-wide with the parameters of its columns in registers and the next row's loads in
 // flight while the current row is reduced.
 //
-// Bound by HBM for many rows: bf16 8192 x 7168 takes 48 us, 4.9 TB/s, where a copy of as many bytes
+// Bound by HBM for many rows: bf16 8192 x 7168 takes 48 to 51 us, 4.6 to 4.9 TB/s, where a copy of as many bytes
 // takes 41 to 48; f32 1531 x 2881 (rows that start at any 4 bytes) 7.9 us of 7.  Few rows are a chain
 // of a load, the sums over the waves and a store: one row of 2880 in 2.7 us, 1.8 us of them the
 // launch.  Not kept: a block per row instead of a walk (57 to 200 us for the 58 that 8192 x 7168 took
