@@ -145,7 +145,8 @@ __global__ __launch_bounds__(kNbWaves<W> * 64) void norm_backward_kernel(
 }
 
 // dweight[h] and dbias[h] = the sums over the P partial rows [P][2H], each wave every 16th row,
-// the waves' sums in wave order.  A block has 64 columns.
+// the waves' sums in wave order.  A block has 64 columns; 32 columns and 32 groups of rows take as
+// long (4.0 us at 4096 x 2880, 4.7 at 8192 x 7168), 16 columns 4.0 and 6.2.
 __global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float* __restrict__ part, int P, int H,
                                                              void* __restrict__ dweight, void* __restrict__ dbias,
                                                              int out_bf16) {
