@@ -134,12 +134,17 @@ __global__ __launch_bounds__(kNbWaves<W> * 64) void norm_backward_kernel(
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = (c * W * kWave + rl) * EL;
+      if (col + EL <= H) {   // in 16-byte stores
+        __builtin_memcpy(pw + col, dw[c], sizeof(dw[c]));
+        __builtin_memcpy(pw + H + col, db[c], sizeof(db[c]));
+      } else {
 #pragma unroll
-      for (int i = 0; i < EL; ++i)
-        if (col + i < H) {
-          pw[col + i] = dw[c][i];
-          pw[H + col + i] = db[c][i];
-        }
+        for (int i = 0; i < EL; ++i)
+          if (col + i < H) {
+            pw[col + i] = dw[c][i];
+            pw[H + col + i] = db[c][i];
+          }
+      }
     }
   }
 }
