@@ -13,13 +13,13 @@
 //
 // mxfp4: e2m1 * 2^s is exact in bf16 (while normal), so the scale is applied while unpacking
 // (v_cvt_scalef32_pk_bf16_fp4).
-// int4: code * scale is not exact in bf16, so the MFMA runs on 128 + code (the nibble put under
-// bf16's 128) and the scale multiplies its f32 result; MFMAs have 32 consecutive channels, all of
-// one scale, after a 4 x 4 transpose of words between the lane groups (v_permlane32_swap,
-// v_permlane16_swap).  The offset leaves as -136 * sum_g scale_g * (sum of the group's
-// activations): in the streaming kernel one 16x16x4 f32 product per four groups of sums that are
-// kept with the activations, in the other a second MFMA with the constant weight -136.  Its terms
-// are at most 17 times the true ones, 2^-24 each.
+// int4: code * scale is not exact in bf16, so the MFMA runs on the codes 0 to 15 and the scale
+// multiplies its f32 result; MFMAs have 32 consecutive channels, all of one scale, after a 4 x 4
+// transpose of words between the lane groups (v_permlane32_swap, v_permlane16_swap).  The offset
+// leaves as -8 * sum_g scale_g * (sum of the group's activations): in the streaming kernel one
+// 16x16x4 f32 product per four groups of sums that are kept with the activations, next to those
+// groups' own products, in the other a second MFMA with the constant weight -8.  The rounded sums
+// have at most (15 + 8) |a| per channel where the true terms have up to 8 |a|.
 
 #include <limits.h>
 
@@ -55,16 +55,22 @@ __device__ __forceinline__ void transpose4(uint32_t (&r)[4]) {
   }
 }
 
-// eight int4 codes -> bf16 128 + code, in the channel order 0 4 1 5 2 6 3 7
+// eight int4 codes -> bf16 0 to 15, in the channel order 0 2 4 6 1 3 5 7: as an e4m3 byte a code
+// is code * 2^-9 (subnormal below 8, and the first binade goes on in the same steps)
 __device__ __forceinline__ uint4 unpack_int4(uint32_t v) {
-  return make_uint4((v & 0x000f000fu) | 0x43004300u, ((v >> 4) & 0x000f000fu) | 0x43004300u,
-                    ((v >> 8) & 0x000f000fu) | 0x43004300u, ((v >> 12) & 0x000f000fu) | 0x43004300u);
+  const uint32_t even = v & 0x0f0f0f0fu, odd = (v >> 4) & 0x0f0f0f0fu;
+  uint4 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, false));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, true));
+  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, false));
+  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, true));
+  return r;
 }
 
 // eight activations into the same order
 __device__ __forceinline__ uint4 order_int4(uint4 a) {
-  return make_uint4(__builtin_amdgcn_perm(a.z, a.x, 0x05040100u), __builtin_amdgcn_perm(a.z, a.x, 0x07060302u),
-                    __builtin_amdgcn_perm(a.w, a.y, 0x05040100u), __builtin_amdgcn_perm(a.w, a.y, 0x07060302u));
+  return make_uint4(__builtin_amdgcn_perm(a.y, a.x, 0x05040100u), __builtin_amdgcn_perm(a.w, a.z, 0x05040100u),
+                    __builtin_amdgcn_perm(a.y, a.x, 0x07060302u), __builtin_amdgcn_perm(a.w, a.z, 0x07060302u));
 }
 
 // eight e2m1 codes -> bf16 code * 2^(e8m0 - 127), in channel order; the conversion takes its scale
@@ -280,14 +286,14 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
     if constexpr (kInt4) {
       // opaque to the compiler, so that each tile makes the offset's products anew: kept for all
       // tiles they would take 4 registers per 32 channels
-      uint32_t c136 = 0xc308c308u;
-      asm volatile("" : "+v"(c136));
-      const bf16x8 b136 = as_bf16x8(make_uint4(c136, c136, c136, c136));
+      uint32_t c8 = 0xc100c100u;   // -8, -8
+      asm volatile("" : "+v"(c8));
+      const bf16x8 b8 = as_bf16x8(make_uint4(c8, c8, c8, c8));
       f32x4 d;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (32 * j % kGroup == 0) d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), b136, d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), b8, d, 0, 0, 0);
         d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), as_bf16x8(unpack_int4(c[j >> 2][j & 3])), d, 0, 0, 0);
         if (32 * (j + 1) % kGroup == 0)
 #pragma unroll
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
     }
   }
   bf16x8 a[S][4];
-  // int4: -136 times the sums of each group's activations, as the first operand of a 16x16x4 product
+  // int4: -8 times the sums of each group's activations, as the first operand of a 16x16x4 product
   // with the scales: lane 16 q + c has row c, group 4 i + q
   float sums[kSums];
   auto load_activations = [&](const RowBlock& b) {
@@ -587,7 +593,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
           for (int i = 0; i < 8; ++i) t += v[i];
           const int g = (s * 128 + 32 * j) / kGroup;
           t = quads_total(t);
-          sums[g / 4] += q == g % 4 ? -136.0f * t : 0.0f;
+          sums[g / 4] += q == g % 4 ? -8.0f * t : 0.0f;
           raw[s][j] = order_int4(raw[s][j]);
         }
         // used here, so that the compiler waits for these loads here and not, with every direct
@@ -666,18 +672,19 @@ __global__ __launch_bounds__(kStreamWaves * 64, (StreamCfg<kInt4, kGroup, S>::kP
     }
     // two sums, so that a product need not wait for the one before it
     f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
-    if constexpr (kInt4) {   // the offsets of all groups
-#pragma unroll
-      for (int i = 0; i < kSums; ++i) {
-        const int g = 4 * i + q;
-        const int from = kGroup > 32 ? sum_from[kGroup > 32 ? i : 0] : scale_from[kGroup > 32 ? 0 : i] + 4 * q;
-        const float f = *reinterpret_cast<const float*>(in + from + shift);
-        const bool there = g < kGroups && wave * S * 128 + g * kGroup < K;
-        acc[i & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(sums[i], there ? f : 0.0f, acc[i & 1], 0, 0, 0);
-      }
-    }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
+      if constexpr (kInt4) {
+        // the offsets of four groups, in front of their products: the sums stay small (all offsets first
+        // would have them start from minus the whole row's)
+        if (s % (kGroup / 32) == 0) {
+          const int i = s / (kGroup / 32), g = 4 * i + q;
+          const int from = kGroup > 32 ? sum_from[kGroup > 32 ? i : 0] : scale_from[kGroup > 32 ? 0 : i] + 4 * q;
+          const float f = *reinterpret_cast<const float*>(in + from + shift);
+          const bool there = g < kGroups && wave * S * 128 + g * kGroup < K;
+          acc[i & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(sums[i], there ? f : 0.0f, acc[i & 1], 0, 0, 0);
+        }
+      }
       const uint4 v = *reinterpret_cast<const uint4*>(in + code_from[s]);
       uint32_t c[4] = {v.x, v.y, v.z, v.w};
       transpose4(c);
