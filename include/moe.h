@@ -413,8 +413,12 @@ moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E,
  *
  *   A            bf16 [A_rows, K].  row(p) = p (A_rows >= M_rows), or with
  *                gather_rows (device int32 [M_rows]) gather_rows[p] /
- *                gather_div clamped into A.  MOE_INT4 needs |A| < 2^120: a row
- *                with a larger or infinite entry may come out as NaN.
+ *                gather_div clamped into A.  MOE_INT4 sums code * A over a group
+ *                before its scale and takes 8 * A off: a row is sure to be right
+ *                if 15 * sum |A| over each group (so |A| <= 2^117) and the sum
+ *                over its groups of 23 * |scale| * sum |A| stay below 2^128.  A
+ *                row with larger or infinite entries may come out as NaN, no
+ *                other row.
  *   codes, scales  4-bit weights [E, N, K], see above; one expert's codes span
  *                under 2 GiB.  K up to 16128 for int4 groups of 32, 32512 for groups
  *                of 64, 65280 otherwise; beyond, MOE_ERR_UNSUPPORTED where a

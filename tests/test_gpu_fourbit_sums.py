@@ -46,3 +46,44 @@ def test_int4_sums_of_large_and_small_activations(group, K):
         rows = slice(off[e], off[e + 1])
         np.testing.assert_array_equal(got[rows], a[rows].double().numpy() @
                                       ofb.dequantize(codes[e].numpy(), scales[e].numpy()).T)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("K", [256, 2048, 7296])
+def test_int4_largest_activations(group, K):
+    """Every activation 2^117, the documented limit of a group of 128: 15 * 128 * 2^117 = 1.875 * 2^127.  With
+    scales of 2^-100 each partial sum is 2^17 times a whole number of at most 23 * 7296 < 2^24: exact."""
+    N = 20
+    gen = torch.Generator().manual_seed(group)
+    codes = torch.randint(0, 256, (1, N, K // 2), generator=gen, dtype=torch.uint8)
+    codes[0, 0], codes[0, 1] = 0, 255                     # every weight -8, every weight 7
+    scales = torch.full((1, N, K // group), 2.0 ** -100)
+    a = torch.full((3, K), 2.0 ** 117, dtype=torch.bfloat16)
+    a[1] = -a[1]
+    say(f"int4 largest activations, groups of {group}, K={K}")
+    got = product(a, codes, scales, [0, 3])
+    np.testing.assert_array_equal(got, a.double().numpy() @ ofb.dequantize(codes[0].numpy(), scales[0].numpy()).T)
+
+
+@pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("int4", 32), ("int4", 128)])
+@pytest.mark.parametrize("K", [512, 7296])
+def test_rows_beside_infinite_and_nan_rows(fmt, group, K):
+    """A row with an infinity or NaN is not finite; the rows beside it keep their bits."""
+    import grouped_gemm_histogram_amd as g
+    gen = torch.Generator().manual_seed(3)
+    N = 24
+    codes = torch.randint(0, 256, (1, N, K // 2), generator=gen, dtype=torch.uint8).to(DEV)
+    if fmt == "mxfp4":
+        scales = torch.randint(118, 124, (1, N, K // 32), generator=gen, dtype=torch.uint8).to(DEV)
+    else:
+        scales = torch.rand(1, N, K // group, generator=gen).to(DEV)
+    a = torch.randn(20, K, generator=gen).to(torch.bfloat16).to(DEV)
+    off = torch.tensor([0, 20], dtype=torch.int32, device=DEV)
+    want = g.grouped_matvec_fourbit(a, codes, scales, off)
+    b = a.clone()
+    b[2, 5], b[18, K - 1], b[19, 0] = float("nan"), float("inf"), -float("inf")
+    got = g.grouped_matvec_fourbit(b, codes, scales, off)
+    bad = torch.zeros(20, dtype=torch.bool, device=DEV)
+    bad[[2, 18, 19]] = True
+    assert torch.equal(got[~bad], want[~bad])
+    assert torch.isnan(got[2]).all() and not torch.isfinite(got[18:]).any()
