@@ -423,7 +423,13 @@ moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E,
  *                under 2 GiB.  K up to 16128 for int4 groups of 32, 32512 for groups
  *                of 64, 65280 otherwise; beyond, MOE_ERR_UNSUPPORTED where a
  *                workgroup's scales do not fit in LDS.
- *                M_rows up to 2^31 - 65.
+ *                M_rows up to 2^31 - 65, and one launch: with B = M_rows/16 +
+ *                min(E, M_rows) + 1 row blocks, B * ceil(N_out/16) (SiLU*up:
+ *                ceil(N_out/8)) up to 2^31 - 1 for K up to 7168 (int4 groups of
+ *                32: 5120), B * ceil(N_out/16) below 2^24 for longer rows (up to
+ *                ceil(N_out/64), SiLU*up ceil(N_out/32), in its place where four
+ *                tiles' scales fit in LDS).  More is MOE_ERR_UNSUPPORTED: call
+ *                on parts of the rows.
  *   offsets      device int32 [E+1], read on the device.  Offsets that do not
  *                ascend are a mistake: no expert has rows then.
  *   epi          as for moe_grouped_gemm (SiLU*up: N even, N_out = N/2).
@@ -431,9 +437,8 @@ moe_status_t moe_quantize_fourbit(const void* w, moe_dtype_t w_dtype, int32_t E,
  *                alignment of its rows needed; rows from offsets[E] on are
  *                written as exact zeros.
  *
- * Any number of rows is computed; the weights are read once per 16 rows of an
- * expert, so with many rows per expert moe_grouped_gemm on bf16 weights is
- * faster.
+ * The weights are read once per 16 rows of an expert, so with many rows per
+ * expert moe_grouped_gemm on bf16 weights is faster.
  * Accumulation is f32, C is rounded once.  mxfp4 values are taken as bf16
  * (exact while they are normal bf16 numbers); int4 values are not rounded at
  * all.
