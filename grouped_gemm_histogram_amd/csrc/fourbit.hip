@@ -204,7 +204,7 @@ __device__ __forceinline__ void stage_scales(const uint8_t* __restrict__ scales,
 // took 349 us where this takes 202 (int4, 128 routes over 256 experts, 7168 x 2048), the streaming
 // kernel 160.
 template <bool kInt4, int kGroup, bool kSilu, int NT>
-__global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p) {
+__global__ __launch_bounds__(kFbWaves * 64, 4) void fourbit_kernel(FourbitArgs p) {
   constexpr int BM = 16;
   constexpr int kCols = (kSilu ? NT / 2 : NT) * 16;   // output columns
   constexpr int kScaleBytes = kInt4 ? 4 : 1;
@@ -289,15 +289,27 @@ __global__ __launch_bounds__(kFbWaves * 64, 2) void fourbit_kernel(FourbitArgs p
       uint32_t c8 = 0xc100c100u;   // -8, -8
       asm volatile("" : "+v"(c8));
       const bf16x8 b8 = as_bf16x8(make_uint4(c8, c8, c8, c8));
-      f32x4 d;
+      // the sums of up to four groups side by side, so that a product need not wait for the one before it: 32 rows
+      // over 8 experts of 28672 x 7424, SiLU * up, take 429 / 260 / 242 us for groups of 32 / 64 / 128, one
+      // group after the other 481 / 281 / 281
+      constexpr int kGroups = kStep / kGroup, kSide = std::min(kGroups, 4);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (32 * j % kGroup == 0) d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), b8, d, 0, 0, 0);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), as_bf16x8(unpack_int4(c[j >> 2][j & 3])), d, 0, 0, 0);
-        if (32 * (j + 1) % kGroup == 0)
+      for (int g0 = 0; g0 < kGroups; g0 += kSide) {
+        f32x4 d[kSide];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(__uint_as_float(s[32 * j / kGroup]), d[i], acc[t][i]);
+        for (int g = 0; g < kSide; ++g) d[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < kGroup / 32; ++h)
+#pragma unroll
+          for (int g = 0; g < kSide; ++g) {
+            const int j = (g0 + g) * (kGroup / 32) + h;
+            d[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), b8, d[g], 0, 0, 0);
+            d[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), as_bf16x8(unpack_int4(c[j >> 2][j & 3])), d[g], 0, 0, 0);
+          }
+#pragma unroll
+        for (int g = 0; g < kSide; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(__uint_as_float(s[g0 + g]), d[g][i], acc[t][i]);
       }
     } else {
 #pragma unroll
