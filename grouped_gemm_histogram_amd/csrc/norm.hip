@@ -141,7 +141,8 @@ template <typename T, bool kVec>
 static hipError_t launch_norm_v(const NormLaunch& p, hipStream_t stream) {
   const int units = (p.H + kRowEl<T> - 1) / kRowEl<T>;
   const NormLauncher<T, kVec> go{p, stream};
-  return p.T < kFewRows ? dispatch_row<1>(units, go) : dispatch_row<16 / kRowEl<T>>(units, go);
+  return p.T < kFewRows ? dispatch_row<1, kWideChunks<T>>(units, go)
+                        : dispatch_row<16 / kRowEl<T>, kWideChunks<T>>(units, go);
 }
 
 template <typename T>

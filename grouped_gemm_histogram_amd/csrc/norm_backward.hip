@@ -211,8 +211,8 @@ static hipError_t launch_norm_backward_t(const NormBackwardLaunch& p, hipStream_
   // 16 waves leave 128 registers (4096 x 8200 takes 80 us for 40, x 12288 119 for 62; narrower rows
   // are equal).  Wider rows do spill: x 16384 140 us, x 20480 477.
   constexpr int kMaxC = sizeof(T) == 2 ? 3 : 4;
-  if (p.H % kRowEl<T> == 0) return dispatch_row<kMaxC>(units, NormBackwardLauncher<T, true>{p, stream});
-  return dispatch_row<kMaxC>(units, NormBackwardLauncher<T, false>{p, stream});
+  if (p.H % kRowEl<T> == 0) return dispatch_row<kMaxC, kWideChunks<T>>(units, NormBackwardLauncher<T, true>{p, stream});
+  return dispatch_row<kMaxC, kWideChunks<T>>(units, NormBackwardLauncher<T, false>{p, stream});
 }
 
 hipError_t launch_norm_backward(const NormBackwardLaunch& p, hipStream_t stream) {

@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "launch.h"
 
 namespace moe {
 
@@ -146,19 +147,22 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int buf, int
 }
 
 // Waves per row and chunks per lane for `units` 16-byte units of a row: the fewest waves that
-// hold it in at most kMaxC chunks a lane, or sixteen waves.
-template <int kMaxC, int W, int C, typename F>
+// hold it in at most kMaxC chunks a lane, or sixteen waves with up to kWideC, the widest row's.
+template <typename T>
+constexpr int kWideChunks = (int)(kNormMaxH / (16 * kWave * kRowEl<T>));
+
+template <int kMaxC, int kWideC, int W, int C, typename F>
 hipError_t dispatch_row_from(int u, F&& f) {
   if (u <= W * C) return f.template operator()<W, C>();
-  if constexpr (C < kMaxC || (W == 16 && C < 8))
-    return dispatch_row_from<kMaxC, W, C + 1>(u, f);
+  if constexpr (W < 16 ? C < kMaxC : C < kWideC)
+    return dispatch_row_from<kMaxC, kWideC, W, C + 1>(u, f);
   else if constexpr (W < 16)
-    return dispatch_row_from<kMaxC, 2 * W, C / 2 + 1>(u, f);
+    return dispatch_row_from<kMaxC, kWideC, 2 * W, C / 2 + 1>(u, f);
   return hipErrorInvalidValue;
 }
-template <int kMaxC, typename F>
+template <int kMaxC, int kWideC, typename F>
 hipError_t dispatch_row(int units, F&& f) {
-  return dispatch_row_from<kMaxC, 1, 1>((units + kWave - 1) / kWave, f);
+  return dispatch_row_from<kMaxC, kWideC, 1, 1>((units + kWave - 1) / kWave, f);
 }
 
 }  // namespace moe
