@@ -158,3 +158,22 @@ def test_same_bits_every_run():
             for _ in range(5):
                 run(other, codes, scales, off, False)
                 assert torch.equal(run(a, codes, scales, off, True, out_dtype=torch.float32), want), (fmt, group, K)
+
+
+@pytest.mark.parametrize("E", [63, 64, 65, 129, 1000, 1024])
+@pytest.mark.parametrize("K", [64, 7424])
+def test_many_experts(E, K):
+    """Up to sixteen experts a lane of the scan, many of them without rows."""
+    gen = torch.Generator().manual_seed(E)
+    counts = torch.randint(0, 40, (E,), generator=gen) * (torch.rand(E, generator=gen) < 0.3)
+    counts[0], counts[-1] = 0, 17
+    off = [0] + torch.cumsum(counts, 0).tolist()
+    M, N = off[-1] + 5, 24
+    say(f"many experts E={E} K={K} rows={M}")
+    for fmt, group in (("mxfp4", 32), ("int4", 64)):
+        codes, scales = weights(E, N, K, fmt, group, E, True)
+        a = torch.randint(-2, 3, (M, K), generator=gen).to(torch.bfloat16).to(DEV)
+        ref, _ = reference(a, codes, scales, off, False, True)
+        out = torch.full((M, N), float("nan"), device=DEV)
+        run(a, codes, scales, off, False, out=out)
+        assert torch.equal(out.double(), ref)
