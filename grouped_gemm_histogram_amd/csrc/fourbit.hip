@@ -200,9 +200,11 @@ __device__ __forceinline__ void stage_scales(const uint8_t* __restrict__ scales,
 // Long weight rows: blocks of 16 rows of an expert, NT weight tiles of 16 rows (with SiLU * up the even
 // ones are gate and the odd ones up).  kGroup: channels per scale (mxfp4: 32).  The waves split K and
 // join their f32 sums in LDS in wave order.  A load instruction takes whole 128-byte lines of 8 weight
-// rows, which `halves` and transpose4 bring into the MFMA's order: lane loads of 64 bytes of 16 rows
-// took 349 us where this takes 202 (int4, 128 routes over 256 experts, 7168 x 2048), the streaming
-// kernel 160.
+// rows, which `halves` and transpose4 bring into the MFMA's order: on rows of 2048, which stream now, lane
+// loads of 64 bytes of 16 rows took 349 us where whole lines took 202 (int4 groups of 128, 128 routes over
+// 256 experts of 7168 x 2048; streamed 166).  8 experts of 4096 x 14336: 64 rows on all of them (250 MB, 40 us
+// at the rate of a read) take 63 us in mxfp4 and 70 in int4 groups of 128, 2 rows on two (62 MB, 10 us) 32 and
+// 38: a wave has one step of its tiles in flight.
 template <bool kInt4, int kGroup, bool kSilu, int NT>
 __global__ __launch_bounds__(kFbWaves * 64, 4) void fourbit_kernel(FourbitArgs p) {
   constexpr int BM = 16;
@@ -376,10 +378,13 @@ static long long fourbit_blocks(long long M_rows, int E) {
 // ---------------------------------------------------------------- rows of up to 7168 channels: streaming
 //
 // Bound by the weights' bytes from HBM: int4 groups of 128, 128 routes over 256 experts of 7168 x 2048
-// take 168 us (789 MB, 4.7 TB/s); int4 groups of 32, 512 routes over 128 of 1536 x 2048, SiLU * up, 59
-// (240 MB, 4.1); mxfp4, 64 routes over 8 of 28672 x 4096 102 (501 MB, 4.9).  One token on four experts
-// of 5760 x 2880, mxfp4 (34 MB) is a chain: 1.8 us launch, 1.2 the experts' scan, 3.4 to the first
-// item's arrival, then 1.7 to 2 us for each of two or three items: 13 us.
+// take 166 us (789 MB, 4.8 TB/s); int4 groups of 32, 512 routes over 128 of 1536 x 2048, SiLU * up, 57
+// (240 MB, 4.2; the VALU is busy 58% of the time, the MFMAs 15%); mxfp4, 64 routes over 8 of 28672 x 4096
+// 103 (501 MB, 4.9).  One token on four experts of 5760 x 2880, mxfp4 (34 MB) is a chain: 1.8 us launch,
+// 1.2 the experts' scan, 3.4 to the first item's arrival, then 1.7 to 2 us for each of two or three
+// items: 13 us.  Each further 16 rows of an expert read and unpack its codes again: 16 / 32 / 64 rows for
+// each of 32 experts of 5760 x 2880, SiLU * up, take 68 / 115 / 196 us in mxfp4, 102 / 168 / 309 in int4
+// groups of 32.
 //
 // A launch is a fixed number of workgroups of eight waves.  Each takes an even share of the items
 // (a block of up to 16 rows of one expert, 16 weight rows; with SiLU * up 8 gate and 8 up rows) in
@@ -393,7 +398,7 @@ static long long fourbit_blocks(long long M_rows, int E) {
 // to the workgroups in turn (174-265 us for 160), all slots filled before the first item instead of all
 // but one (one token 14.1 us for 13.1).  More than 16 rows per expert: 32- and 64-row blocks in the
 // other kernel, which read the weights fewer times, took 107 / 192 / 314 and 169 / 212 / 351 us at
-// 16 / 32 / 64 rows per expert where this takes 80 / 128 / 211 (mxfp4, 32 experts, 5760 x 2880).
+// 16 / 32 / 64 rows per expert where this took 80 / 128 / 211 beside them (mxfp4, 32 experts, 5760 x 2880).
 //
 // A weight row's 16-byte pieces lie in its LDS row in the order piece ^ swizzle, chosen so that the
 // 16 lanes that read one piece of 16 rows hit different banks.
@@ -834,6 +839,8 @@ hipError_t launch_fourbit(const FourbitLaunch& p, hipStream_t stream) {
 //   int4:  scale = amax / 7 (1 if that is zero), code = 8 + round(w / scale)
 //   mxfp4: scale = 2^(floor(log2 amax) - 2), code = w / scale in e2m1; ties to the even code,
 //          magnitudes past 6 give 6
+// Bound by HBM: 32 x 5760 x 2880 to mxfp4 takes 337 us from bf16 (1.34 GB, 4.0 TB/s), 411 from f32 (2.40 GB,
+// 5.8); x 2816 to int4 groups of 128 333 and 399.
 template <bool kInt4, int kGroup, bool kBf16In>
 __global__ __launch_bounds__(256) void quantize_fourbit_kernel(const void* __restrict__ w_, long long n8,
                                                                uint32_t* __restrict__ codes, void* __restrict__ scales) {

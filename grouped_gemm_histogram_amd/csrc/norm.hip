@@ -9,10 +9,12 @@
 // flight while the current row is reduced.
 //
 // Bound by HBM for many rows: bf16 8192 x 7168 takes 48 to 51 us, 4.6 to 4.9 TB/s, where a copy of as many bytes
-// takes 41 to 48; f32 1531 x 2881 (rows that start at any 4 bytes) 7.9 us of 7.  Few rows are a chain
-// of a load, the sums over the waves and a store: one row of 2880 in 2.7 us, 1.8 us of them the
-// launch.  Not kept: a block per row instead of a walk (57 to 200 us for the 58 that 8192 x 7168 took
-// before the parameters came in 16-byte loads), two or four rows per barrier (no gain).
+// takes 41 to 48 (with 23 VALU operations an element, the VALU is busy 87% of the time); f32 1531 x 2881
+// (rows that start at any 4 bytes) 7.9 us of 7.  Few rows are a chain of a load, the sums over the waves
+// and a store: one row of 2880 in 2.5 us, 1.8 us of them the launch.  Rows that need four chunks a lane
+// of bf16 or seven of f32 in sixteen waves (over 24576 elements) spill registers: bf16 4096 x 28672
+// takes 163 us, 2.9 TB/s.  Not kept: a block per row instead of a walk (57 to 200 us for the 58 that
+// 8192 x 7168 took before the parameters came in 16-byte loads), two or four rows per barrier (no gain).
 
 #include <algorithm>
 
@@ -128,7 +130,7 @@ struct NormLauncher {
     constexpr int kWaves = kNormWaves<W>;
     constexpr int kSlots = kWaves / W;
     const long long blocks = (p.T + kSlots - 1) / kSlots;
-    // 16 waves a CU: 8, 24 and 40 take 71, 64 and 69 us where this takes 58 (as above)
+    // 16 waves a CU: 8, 24 and 40 took 71, 64 and 69 us where 16 took 58 (8192 x 7168, as above)
     const unsigned grid = (unsigned)std::min<long long>(blocks, 256 * 16 / kWaves);
     hipLaunchKernelGGL((norm_kernel<T, kVec, W, C>), dim3(grid), dim3(kWaves * kWave), 0, stream,
                        static_cast<const T*>(p.x), p.T, p.H, p.weight, p.bias, p.w_bf16, p.eps, p.rms,

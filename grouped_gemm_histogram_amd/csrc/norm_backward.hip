@@ -9,11 +9,12 @@
 // registers until the block's last row.  The sums go to the workspace, one row per row slot, and
 // a second kernel adds those rows in a fixed order: no atomics, so results do not vary.
 //
-// Bound by HBM: x and dy read, dx written.  bf16 8192 x 7168 takes 68 us (5.2 TB/s) and 4.7 for the
-// sums of the partial rows; 4096 x 2880 18 and 4.0, where its 71 MB alone would take 12 to 14: with
-// 16 rows a block, filling and draining the pipeline and the columns' sums show.  Two, three and four
-// rows' loads in flight ahead of the current row's sums are slower than one (by 0.9, 1.9 and 2.9 us).
-// The columns' sums stored word by word cost 2 to 3 us more.
+// Bound by HBM: x and dy read, dx written.  bf16 8192 x 7168 takes 68 us (5.2 TB/s) and 5.0 for the
+// sums of the partial rows; 4096 x 2880 17 and 4.0 (f32 26 and 4.0), where its 71 MB alone would take 12
+// to 14: with 16 rows a block, filling and draining the pipeline and the columns' sums show.  One row of
+// 2880 takes 5.1 and 2.3.  The columns' sums of both gradients are made also where only one is asked for.
+// Two, three and four rows' loads in flight ahead of the current row's sums are slower than one (by 0.9, 1.9
+// and 2.9 us).  The columns' sums stored word by word cost 2 to 3 us more.
 
 #include <algorithm>
 
@@ -208,8 +209,8 @@ template <typename T>
 static hipError_t launch_norm_backward_t(const NormBackwardLaunch& p, hipStream_t stream) {
   const int units = (p.H + kRowEl<T> - 1) / kRowEl<T>;
   // chunks a lane before a row takes more waves.  Three of bf16: two spill from 8192 elements on, where
-  // 16 waves leave 128 registers (4096 x 8200 takes 80 us for 40, x 12288 119 for 62; narrower rows
-  // are equal).  Wider rows do spill: x 16384 140 us, x 20480 477.
+  // 16 waves leave 128 registers (4096 x 8200 takes 80 us for 39, x 12288 119 for 59; narrower rows
+  // are equal).  Wider rows do spill: x 16384 145 us, x 20480 470, f32 2048 x 16384 140.
   constexpr int kMaxC = sizeof(T) == 2 ? 3 : 4;
   if (p.H % kRowEl<T> == 0) return dispatch_row<kMaxC, kWideChunks<T>>(units, NormBackwardLauncher<T, true>{p, stream});
   return dispatch_row<kMaxC, kWideChunks<T>>(units, NormBackwardLauncher<T, false>{p, stream});

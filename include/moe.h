@@ -46,7 +46,8 @@
  *    message for the last non-OK status.
  *  - Limits: 1 <= E <= 1024, 1 <= k <= min(E, 16), R = T*k < 2^31.
  *  - Results are deterministic: repeated calls on the same inputs give
- *    bitwise-identical outputs (no floating-point atomics, no split-K).
+ *    bitwise-identical outputs (no floating-point atomics; sums that several
+ *    waves share are joined in a fixed order).
  */
 #ifndef MOE_H_
 #define MOE_H_
