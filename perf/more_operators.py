@@ -22,6 +22,8 @@ _DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 _BYTES = {"bf16": 2, "f32": 4}
 # elements that share a scale of an 8-bit optimizer state; tensors start at multiples of it
 BLOCK = 128
+# rows and blocks whose largest value is below this are held as zeros: 448 over it is still finite
+TINY = 2.0 ** -100
 
 # the values of the sixteen 4-bit floating codes (1 sign, 2 exponent, 1 mantissa bit)
 _E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0]
@@ -113,10 +115,11 @@ def _randn(g, *shape):
 
 
 def _quantise_rows(x):
-    """8-bit codes and a scale for each row: scale = amax / 127 (1 for a row of zeros), code = round(x * (127 / amax))."""
+    """8-bit codes and a scale for each row: scale = amax / 127, code = round(x * (127 / amax)); a row
+    below TINY counts as zeros, with scale 1."""
     x = x.float()
     amax = x.abs().amax(dim=-1)
-    some = amax > 0
+    some = amax >= TINY
     scale = torch.where(some, amax / 127.0, torch.ones_like(amax))
     inv = torch.where(some, 127.0 / amax, torch.zeros_like(amax))
     return torch.round(x * inv[..., None]).to(torch.int8), scale
@@ -199,7 +202,7 @@ def _prepare_adamw(case, g, st, seed):
         for name, x in (("m", m), ("v", u)):
             b = x.view(-1, BLOCK)
             amax = b.abs().amax(dim=1)
-            s = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+            s = torch.where(amax >= TINY, amax / 448.0, torch.ones_like(amax))
             st[name] = (b / s[:, None]).clamp(-448, 448).view(-1).to(torch.float8_e4m3fn)
             st[name + "_scale"] = s
     else:
@@ -400,7 +403,7 @@ def _plain_adamw(st):
         for name, x in (("m", m), ("v", u)):
             b = x.view(-1, BLOCK)
             amax = b.abs().amax(dim=1)
-            some = amax > 0
+            some = amax >= TINY
             scale = torch.where(some, amax / 448.0, torch.ones_like(amax))
             inv = torch.where(some, 448.0 / amax, torch.zeros_like(amax))
             q = (b * inv[:, None]).clamp(-448.0, 448.0).view(-1)
@@ -430,11 +433,11 @@ def _run_own(st):
     op = case["op"]
     if op == "gemm":
         more = dict(gather_rows=st["sorted_rows"], gather_div=case["k"]) if case["silu"] else {}
-        return g.grouped_gemm_int8(st["a"], st["a_scale"], st["b"], st["b_scale"], st["offsets"],
-                                   "silu_mul" if case["silu"] else "none", out_dtype=_DT[case["out"]], **more)
+        return g.grouped_gemm_eightbit(st["a"], st["a_scale"], st["b"], st["b_scale"], st["offsets"],
+                                       "silu_mul" if case["silu"] else "none", out_dtype=_DT[case["out"]], **more)
     if op == "layer8":
-        return g.forward_int8(st["x"], st["logits"], st["w13"], st["w13_scale"], st["w2"], st["w2_scale"], case["k"],
-                              num_valid_rows=st["valid"])
+        return g.forward_eightbit(st["x"], st["logits"], st["w13"], st["w13_scale"], st["w2"], st["w2_scale"],
+                                  case["k"], num_valid_rows=st["valid"])
     if op == "decode":
         return g.forward_decode(st["x"], st["logits"], st["w13"], st["w2"], case["k"], num_valid_rows=st["valid"],
                                 w13_scale=st["w13_scale"], w2_scale=st["w2_scale"])
@@ -515,8 +518,8 @@ def _exact_codes(x):
     """Dequantised rows of the 8-bit quantiser, whose decisions are taken in 32 bits."""
     x = x.float()
     top = x.abs().max(dim=1, keepdim=True).values
-    inv = torch.where(top > 0, 127.0 / top, torch.zeros_like(top))
-    step = torch.where(top > 0, top / 127.0, torch.ones_like(top))
+    inv = torch.where(top >= TINY, 127.0 / top, torch.zeros_like(top))
+    step = torch.where(top >= TINY, top / 127.0, torch.ones_like(top))
     return (x * inv).round().double() * step.double()
 
 
@@ -602,7 +605,7 @@ def _exact_adamw(case, st):
     if small:
         for name, x in (("m", m), ("v", torch.sqrt(v))):
             top = x.view(-1, BLOCK).abs().max(dim=1).values
-            scale = torch.where(top > 0, top / 448.0, torch.ones_like(top))
+            scale = torch.where(top >= TINY, top / 448.0, torch.ones_like(top))
             q = (x.view(-1, BLOCK) / scale[:, None]).view(-1)
             if piece is not None:
                 q = _exact_round(q, piece, 3, -6, 0.5)
