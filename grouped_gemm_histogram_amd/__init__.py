@@ -9,9 +9,15 @@ loads ``libmoe.so``; ``build`` compiles it.
 
 from ._lib import MoeKernels, load  # noqa: F401
 from .ops import (  # noqa: F401
+    AdamWState,
     Gradients,
     NormGradients,
     NormStats,
+    adamw_counters,
+    adamw_init,
+    adamw_schedule,
+    adamw_starts,
+    adamw_step,
     backward,
     backward_workspace_bytes,
     build_offsets,
@@ -20,10 +26,13 @@ from .ops import (  # noqa: F401
     dropout_add_backward,
     dropout_counters,
     forward,
+    forward_eightbit,
+    forward_eightbit_workspace_bytes,
     forward_fourbit,
     forward_fourbit_workspace_bytes,
     forward_workspace_bytes,
     grouped_gemm,
+    grouped_gemm_eightbit,
     grouped_gemm_gather,
     grouped_gemm_tile_shape,
     grouped_matvec_fourbit,
@@ -33,6 +42,7 @@ from .ops import (  # noqa: F401
     permute,
     quantize_fourbit,
     quantize_rows,
+    quantize_rows_eightbit,
     route_topk,
     unpermute_combine,
     unpermute_combine_dropout,

@@ -35,6 +35,10 @@ class MoeAux(ctypes.Structure):
                 ("sorted_rows", P), ("row_pos", P), ("stage_events", ctypes.POINTER(P))]
 
 
+class MoeAdamw(ctypes.Structure):
+    _fields_ = [("lr", F64), ("beta1", F64), ("beta2", F64), ("eps", F64), ("weight_decay", F64), ("step", I64)]
+
+
 # stage 3: nothing for f32/bf16 layers (the gate/up GEMM gathers token rows); per-token
 # quantisation for fp8
 FORWARD_STAGES = ("route", "offsets", "act_staging", "gemm_gate_up", "gemm_down", "combine")
@@ -65,11 +69,18 @@ SIGNATURES: dict[str, tuple] = {
     "moe_forward_fourbit_workspace": (SZ, [I64, I64, I64, I32, I32]),
     "moe_forward_fourbit": (I32, [P, P, P, P, P, P, I32, I32, I64, I64, I64, I32, I32, I64, I32, P, I32,
                                   ctypes.POINTER(MoeAux), P, SZ, P]),
+    "moe_quantize_rows_eightbit": (I32, [P, I32, I64, I64, P, P, P]),
+    "moe_grouped_gemm_eightbit": (I32, [P, P, I64, P, I32, P, P, P, I32, I64, I64, I64, I32, P, I32, P]),
+    "moe_forward_eightbit_workspace": (SZ, [I64, I64, I64, I32, I32]),
+    "moe_forward_eightbit": (I32, [P, P, P, P, P, P, I64, I64, I64, I32, I32, I64, I32, P, I32,
+                                   ctypes.POINTER(MoeAux), P, SZ, P]),
     "moe_layer_norm": (I32, [P, I32, I64, I64, P, P, I32, F32, I32, P, P, P, P]),
     "moe_layer_norm_backward_workspace": (SZ, [I64, I64]),
     "moe_layer_norm_backward": (I32, [P, P, I32, I64, I64, P, I32, P, P, I32, P, P, P, I32, P, SZ, P]),
     "moe_dropout_add": (I32, [P, I32, P, I32, I64, F64, P, P, I32, P]),
     "moe_unpermute_combine_dropout": (I32, [P, I32, P, P, P, I32, I64, I64, I32, P, I32, F64, P, P, I32, P]),
+    "moe_adamw_state_elements": (I64, [P, I64]),
+    "moe_adamw_step": (I32, [P, P, P, I64, I32, I32, I32, P, P, P, P, P, ctypes.POINTER(MoeAdamw), P, P, P, P]),
     "moe_status_string": (ctypes.c_char_p, [I32]),
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_abi_version": (I32, []),
@@ -96,11 +107,17 @@ class MoeKernels:
     grouped_matvec_fourbit: Callable
     forward_fourbit_workspace: Callable
     forward_fourbit: Callable
+    quantize_rows_eightbit: Callable
+    grouped_gemm_eightbit: Callable
+    forward_eightbit_workspace: Callable
+    forward_eightbit: Callable
     layer_norm: Callable
     layer_norm_backward_workspace: Callable
     layer_norm_backward: Callable
     dropout_add: Callable
     unpermute_combine_dropout: Callable
+    adamw_state_elements: Callable
+    adamw_step: Callable
     status_string: Callable
     last_error: Callable
     abi_version: Callable

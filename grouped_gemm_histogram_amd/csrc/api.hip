@@ -913,6 +913,208 @@ moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, cons
   return ok();
 }
 
+// ------------------------------------------------------------------------- 8-bit weights
+
+}  // extern "C"
+
+namespace {
+
+// |sum of K products of codes| <= 2^14 K stays below 2^31
+constexpr long long kEightbitMaxK = 131056;
+
+struct EightbitLayout {
+  size_t ids, w, offsets, sorted, rowpos, offws, xq, xs, h, hq, hs, y, total;
+};
+
+EightbitLayout eightbit_layout(long long T, long long H, long long I, int E, int k) {
+  const long long R = T * k;
+  EightbitLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.ids = take(R * 4);
+  L.w = take(R * 4);
+  L.offsets = take((E + 1) * 4);
+  L.sorted = take(R * 4);
+  L.rowpos = take(R * 4);
+  L.offws = take(std::max(moe::build_offsets_workspace_bytes(R, E), moe::route_offsets_workspace_bytes(T, E)));
+  L.xq = take(T * H);
+  L.xs = take(T * 4);
+  L.h = take(R * I * 2);
+  L.hq = take(R * I);
+  L.hs = take(R * 4);
+  L.y = take(R * H * 2);
+  L.total = off;
+  return L;
+}
+
+// What moe_forward_eightbit refuses in its sizes; MOE_OK when it takes them.
+moe_status_t check_eightbit_sizes(long long T, long long H, long long I, int E, int k) {
+  if (moe_status_t s = check_experts(E, k)) return s;
+  MOE_REQUIRE(T >= 0 && T <= kMaxRows && T * k <= kMaxRows && H > 0 && I > 0 && H <= kMaxRows && I <= kMaxRows,
+              "bad sizes");
+  MOE_REQUIRE(H % 16 == 0 && I % 16 == 0, "H=%lld and I=%lld must be multiples of 16", H, I);
+  if (H > moe::kNormMaxH || I > moe::kNormMaxH)
+    return fail(MOE_ERR_UNSUPPORTED, "rows of more than %lld elements are not quantised", (long long)moe::kNormMaxH);
+  MOE_REQUIRE(T * H <= (long long)UINT32_MAX && T * k * I <= (long long)UINT32_MAX,
+              "token rows and the quantised hidden rows must each span under 4 GiB");
+  return MOE_OK;   // one expert's weights: 2 * 32768^2 bytes at most
+}
+
+moe_status_t grouped_gemm_eightbit_impl(const void* A, const float* a_scales, long long A_rows, const int32_t* gather_rows,
+                                        int32_t gather_div, const void* B, const float* b_scales, const int32_t* offsets,
+                                        int32_t E, long long M_rows, long long N, long long K, moe_epilogue_t epi, void* C,
+                                        moe_dtype_t c_dtype, void* stream, long long tile_rows) {
+  MOE_REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "E=%d outside [1, %d]", E, MOE_MAX_EXPERTS);
+  MOE_REQUIRE(epi == MOE_EPI_NONE || epi == MOE_EPI_SILU_MUL, "bad epilogue");
+  MOE_REQUIRE(f32_or_bf16(c_dtype), "c_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(M_rows >= 0 && M_rows <= kMaxRows && A_rows >= 0 && A_rows <= kMaxRows && N > 0 && N <= kMaxRows && K > 0,
+              "bad sizes");
+  MOE_REQUIRE(K % 16 == 0, "K=%lld is not a multiple of 16", K);
+  if (K > kEightbitMaxK)
+    return fail(MOE_ERR_UNSUPPORTED, "K=%lld: sums of more than %lld products may pass 32 bits", K, kEightbitMaxK);
+  const bool silu = epi == MOE_EPI_SILU_MUL;
+  MOE_REQUIRE(!silu || N % 2 == 0, "SiLU*up needs an even N");
+  const long long N_out = silu ? N / 2 : N;
+  MOE_REQUIRE((N_out * esize(c_dtype)) % 16 == 0, "rows of C must be a multiple of 16 bytes");
+  if (gather_rows)
+    MOE_REQUIRE(gather_div >= 1 && gather_div <= MOE_MAX_TOPK, "gather_div=%d outside [1, %d]", gather_div, MOE_MAX_TOPK);
+  else
+    MOE_REQUIRE(A_rows >= M_rows, "A has %lld rows but the product has %lld", A_rows, M_rows);
+  MOE_REQUIRE(A_rows * K <= (long long)UINT32_MAX, "A must span under 4 GiB");
+  MOE_REQUIRE(N * K <= (long long)UINT32_MAX, "one expert's B must span under 4 GiB");
+  if (M_rows == 0) return ok();
+  MOE_REQUIRE(A_rows > 0, "A has no rows but the product has %lld", M_rows);
+  MOE_REQUIRE(A && a_scales && B && b_scales && offsets && C, "null pointer argument");
+  MOE_REQUIRE(aligned16(A) && aligned16(B) && aligned16(C) && aligned16(b_scales),
+              "A, B, b_scales and C must be 16-byte aligned");
+  MOE_REQUIRE(aligned_to(a_scales, 4), "a_scales must be 4-byte aligned");
+  moe::GemmLaunch p{};
+  p.A = A;
+  p.a_scales = a_scales;
+  p.a_rows = gather_rows;
+  p.a_div = gather_div;
+  p.a_total = A_rows;
+  p.B = B;
+  p.b_scales = b_scales;
+  p.ab_dtype = 3;
+  p.offsets = offsets;
+  p.E = E;
+  p.M_rows = M_rows;
+  p.N = N;
+  p.K = K;
+  p.silu = silu;
+  p.C = C;
+  p.c_dtype = c_dtype;
+  p.tile_rows = tile_rows;
+  return launched(moe::launch_grouped_gemm(p, as_stream(stream)), "grouped_gemm_eightbit");
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_quantize_rows_eightbit(const void* x, moe_dtype_t x_dtype, int64_t rows, int64_t H, void* codes,
+                                        float* scales, void* stream) {
+  MOE_REQUIRE(f32_or_bf16(x_dtype), "x_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(rows >= 0 && rows <= kMaxRows && H > 0, "bad sizes");
+  MOE_REQUIRE(H % 16 == 0, "H=%lld is not a multiple of 16", (long long)H);
+  if (H > moe::kNormMaxH)
+    return fail(MOE_ERR_UNSUPPORTED, "H=%lld exceeds %lld", (long long)H, (long long)moe::kNormMaxH);
+  if (rows == 0) return ok();
+  MOE_REQUIRE(x && codes && scales, "null pointer argument");
+  MOE_REQUIRE(aligned16(x) && aligned16(codes), "x and codes must be 16-byte aligned");
+  MOE_REQUIRE(aligned_to(scales, 4), "scales must be 4-byte aligned");
+  moe::QuantizeLaunch p{};
+  p.x = x;
+  p.x_bf16 = x_dtype == MOE_BF16;
+  p.rows = rows;
+  p.H = (int)H;
+  p.codes = codes;
+  p.scales = scales;
+  return launched(moe::launch_quantize_eightbit(p, as_stream(stream)), "quantize_rows_eightbit");
+}
+
+moe_status_t moe_grouped_gemm_eightbit(const void* A, const float* a_scales, int64_t A_rows, const int32_t* gather_rows,
+                                       int32_t gather_div, const void* B, const float* b_scales, const int32_t* offsets,
+                                       int32_t E, int64_t M_rows, int64_t N, int64_t K, moe_epilogue_t epi, void* C,
+                                       moe_dtype_t c_dtype, void* stream) {
+  return grouped_gemm_eightbit_impl(A, a_scales, A_rows, gather_rows, gather_div, B, b_scales, offsets, E, M_rows, N, K,
+                                    epi, C, c_dtype, stream, 0);
+}
+
+size_t moe_forward_eightbit_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+  if (check_eightbit_sizes(T, H, I, E, k)) return 0;   // moe_forward_eightbit rejects it
+  return eightbit_layout(T, H, I, E, k).total;
+}
+
+moe_status_t moe_forward_eightbit(const void* x, const float* router_logits, const void* w13, const float* w13_scales,
+                                  const void* w2, const float* w2_scales, int64_t T, int64_t H, int64_t I, int32_t E,
+                                  int32_t k, int64_t num_valid_rows, int32_t renormalize, void* out,
+                                  moe_dtype_t out_dtype, moe_aux_t* aux, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (moe_status_t s = check_eightbit_sizes(T, H, I, E, k)) return s;
+  MOE_REQUIRE(f32_or_bf16(out_dtype), "out_dtype must be MOE_F32 or MOE_BF16");
+  if (T > 0) {
+    MOE_REQUIRE(x && router_logits && w13 && w13_scales && w2 && w2_scales && out, "null pointer argument");
+    MOE_REQUIRE(aligned16(x) && aligned16(w13) && aligned16(w13_scales) && aligned16(w2) && aligned16(w2_scales) &&
+                    aligned16(out),
+                "x, weights, scales and out must be 16-byte aligned");
+  }
+  const EightbitLayout L = eightbit_layout(T, H, I, E, k);
+  if (!workspace || workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, L.total);
+  MOE_REQUIRE(aligned16(workspace), "workspace must be 16-byte aligned");
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const Routing r{(aux && aux->topk_ids) ? aux->topk_ids : reinterpret_cast<int32_t*>(ws + L.ids),
+                  (aux && aux->topk_weights) ? aux->topk_weights : reinterpret_cast<float*>(ws + L.w),
+                  (aux && aux->offsets) ? aux->offsets : reinterpret_cast<int32_t*>(ws + L.offsets),
+                  (aux && aux->sorted_rows) ? aux->sorted_rows : reinterpret_cast<int32_t*>(ws + L.sorted),
+                  (aux && aux->row_pos) ? aux->row_pos : reinterpret_cast<int32_t*>(ws + L.rowpos)};
+  const StageEvents mark{aux ? aux->stage_events : nullptr, stream};
+  moe_status_t s;
+  if ((s = route_stages(router_logits, T, E, k, num_valid_rows, renormalize, r, ws + L.offws, mark, stream))) return s;
+  if (T == 0) {
+    for (int i = 3; i <= MOE_FORWARD_STAGES; ++i)
+      if ((s = mark(i))) return s;
+    return ok();
+  }
+  float* xs = reinterpret_cast<float*>(ws + L.xs);
+  float* hs = reinterpret_cast<float*>(ws + L.hs);
+  if ((s = moe_quantize_rows_eightbit(x, MOE_BF16, T, H, ws + L.xq, xs, stream))) return s;
+  if ((s = mark(3))) return s;
+  // tiles are chosen for the rows that can be valid, as in moe_forward
+  const long long R = T * k;
+  const long long V_host = (num_valid_rows >= 0 && num_valid_rows < R) ? num_valid_rows : R;
+  const long long tile_rows = V_host > 0 ? V_host : 1;
+  if ((s = grouped_gemm_eightbit_impl(ws + L.xq, xs, T, r.sorted, k, w13, w13_scales, r.offsets, E, R, 2 * I, H,
+                                      MOE_EPI_SILU_MUL, ws + L.h, MOE_BF16, stream, tile_rows)))
+    return s;
+  moe::QuantizeLaunch q{};   // a row's scale needs its largest value: a pass over the valid rows of h
+  q.x = ws + L.h;
+  q.x_bf16 = true;
+  q.rows = R;
+  q.valid = r.offsets + E;
+  q.H = (int)I;
+  q.codes = ws + L.hq;
+  q.scales = hs;
+  if ((s = launched(moe::launch_quantize_eightbit(q, as_stream(stream)), "quantize_rows_eightbit"))) return s;
+  if ((s = mark(4))) return s;
+  if ((s = grouped_gemm_eightbit_impl(ws + L.hq, hs, R, nullptr, 1, w2, w2_scales, r.offsets, E, R, H, I, MOE_EPI_NONE,
+                                      ws + L.y, MOE_BF16, stream, tile_rows)))
+    return s;
+  if ((s = mark(5))) return s;
+  if ((s = moe_unpermute_combine(ws + L.y, MOE_BF16, r.rowpos, r.weights, r.offsets, E, T, H, k, out, out_dtype,
+                                 stream)))
+    return s;
+  if ((s = mark(6))) return s;
+  return ok();
+}
+
 // ------------------------------------------------------------------------- norm and dropout
 
 moe_status_t moe_layer_norm(const void* x, moe_dtype_t x_dtype, int64_t T, int64_t H, const void* weight,
@@ -1010,6 +1212,78 @@ moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, c
   return launched(moe::launch_combine_dropout(y, y_dtype == MOE_BF16, row_pos, topk_weights, offsets, E, (int)T,
                                               (int)H, k, drop, out, out_dtype == MOE_BF16, as_stream(stream)),
                   "unpermute_combine_dropout");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------- optimizer
+
+extern "C" {
+
+int64_t moe_adamw_state_elements(const int64_t* n, int64_t count) {
+  if (count < 0 || (count > 0 && !n)) return -1;
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (n[i] < 0 || n[i] > (1ll << 40) || total > (1ll << 48)) return -1;
+    total += (n[i] + 127) & ~127ll;
+  }
+  return total;
+}
+
+moe_status_t moe_adamw_step(void* const* params, const void* const* grads, const int64_t* n, int64_t count,
+                            moe_dtype_t p_dtype, moe_dtype_t g_dtype, moe_dtype_t state_dtype, void* m, float* m_scale,
+                            void* v, float* v_scale, float* master, const moe_adamw_t* hyper, const float* schedule,
+                            const float* grad_scale, const uint64_t* rng, void* stream) {
+  MOE_REQUIRE(f32_or_bf16(p_dtype) && f32_or_bf16(g_dtype), "p_dtype and g_dtype must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(state_dtype == MOE_F32 || state_dtype == MOE_FP8_E4M3, "state_dtype must be MOE_F32 or MOE_FP8_E4M3");
+  MOE_REQUIRE(hyper, "hyper is null");
+  const moe_adamw_t& h = *hyper;
+  MOE_REQUIRE(isfinite(h.lr) && h.lr >= 0 && isfinite(h.weight_decay) && h.weight_decay >= 0,
+              "lr=%g and weight_decay=%g must be finite and not negative", h.lr, h.weight_decay);
+  MOE_REQUIRE(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1, "beta1=%g and beta2=%g must be in [0, 1)",
+              h.beta1, h.beta2);
+  MOE_REQUIRE(isfinite(h.eps) && h.eps >= 1e-30, "eps=%g must be finite and at least 1e-30", h.eps);
+  MOE_REQUIRE(h.step >= 1, "step=%lld is not at least 1", (long long)h.step);
+  const int64_t total = moe_adamw_state_elements(n, count);
+  MOE_REQUIRE(total >= 0, "bad count or sizes");
+  if (total == 0) return ok();
+  const bool s8 = state_dtype == MOE_FP8_E4M3;
+  MOE_REQUIRE(params && grads && m && v, "null pointer argument");
+  MOE_REQUIRE(!s8 || (m_scale && v_scale), "8-bit states need m_scale and v_scale");
+  MOE_REQUIRE(!master || p_dtype == MOE_BF16, "master is the f32 copy of bf16 params");
+  MOE_REQUIRE(aligned16(m) && aligned16(v) && aligned16(master), "states must be 16-byte aligned");
+  MOE_REQUIRE(aligned_to(m_scale, 4) && aligned_to(v_scale, 4) && aligned_to(schedule, 4) && aligned_to(grad_scale, 4),
+              "scales and schedule must be 4-byte aligned");
+  MOE_REQUIRE(aligned_to(rng, 8), "rng must be 8-byte aligned");
+  for (int64_t i = 0; i < count; ++i) {
+    if (n[i] == 0) continue;
+    MOE_REQUIRE(params[i] && grads[i], "params[%lld] or grads[%lld] is null", (long long)i, (long long)i);
+    MOE_REQUIRE(aligned16(params[i]) && aligned16(grads[i]), "params[%lld] and grads[%lld] must be 16-byte aligned",
+                (long long)i, (long long)i);
+  }
+  moe::AdamwLaunch q{};
+  q.count = count;
+  q.param = params;
+  q.grad = grads;
+  q.n = n;
+  q.p_bf16 = p_dtype == MOE_BF16;
+  q.g_bf16 = g_dtype == MOE_BF16;
+  q.s8 = s8;
+  q.m = m;
+  q.v = v;
+  q.m_scale = m_scale;
+  q.v_scale = v_scale;
+  q.master = master;
+  q.lr = h.lr;
+  q.beta1 = h.beta1;
+  q.beta2 = h.beta2;
+  q.eps = h.eps;
+  q.weight_decay = h.weight_decay;
+  q.step = h.step;
+  q.schedule = schedule;
+  q.grad_scale = grad_scale;
+  q.rng = rng;
+  return launched(moe::launch_adamw(q, as_stream(stream)), "adamw_step");
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@ constexpr int kWave = 64;
 
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
+typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
 typedef __attribute__((__vector_size__(8 * sizeof(int)))) int i32x8;
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & (kWave - 1); }

@@ -50,7 +50,7 @@
 
 namespace moe {
 
-enum class AbType { F32, BF16, FP8 };
+enum class AbType { F32, BF16, FP8, I8 };
 enum class CType { F32, BF16, FP8 };
 
 template <AbType T> struct AbTraits;
@@ -62,6 +62,10 @@ template <> struct AbTraits<AbType::F32> {
 };
 template <> struct AbTraits<AbType::FP8> {
   static constexpr int kEsize = 1, kSteps = 1, kChunksPerLane = 2;
+};
+// 8-bit integers: a 64-deep MFMA reads as many bytes a lane as bf16's 32-deep one, so both share the loop
+template <> struct AbTraits<AbType::I8> {
+  static constexpr int kEsize = 1, kSteps = 2, kChunksPerLane = 1;
 };
 
 struct GemmArgs {
@@ -184,6 +188,16 @@ constexpr int kMaxExperts = 1024;
 #endif
 #ifndef MOE_DECODE_NARROW_ROWS_PER_EXPERT
 #define MOE_DECODE_NARROW_ROWS_PER_EXPERT 2
+#endif
+// 8-bit integers
+#ifndef MOE_TILE_I8
+#define MOE_TILE_I8 192, 192, 4, 2, 0, 3
+#endif
+#ifndef MOE_TILE_I8_MID
+#define MOE_TILE_I8_MID 32, 64, 2, 2, 0, 6
+#endif
+#ifndef MOE_TILE_I8_DEC
+#define MOE_TILE_I8_DEC 16, 32, 1, 1, 0, 8
 #endif
 #ifndef MOE_TILE_FP8_NONE
 #define MOE_TILE_FP8_NONE 128, 256, 2, 4, 0, 3
@@ -552,11 +566,12 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_gemm_kernel(GemmArgs args
             masked(rb[i]);
     };
 
-    f32x4 acc[SM][SNB];
+    using AccT = std::conditional_t<AB == AbType::I8, i32x4, f32x4>;   // integer sums are exact
+    AccT acc[SM][SNB];
 #pragma unroll
     for (int t = 0; t < SM; ++t)
 #pragma unroll
-      for (int s = 0; s < SNB; ++s) acc[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < SNB; ++s) acc[t][s] = AccT{0, 0, 0, 0};
 
     // Activation subtile t of wave wm holds tile rows 16*(t*WM + wm) + [0, 16): the
     // waves of a column interleave, so a short tile still spreads over all of them.
@@ -709,7 +724,7 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_gemm_kernel(GemmArgs args
         };
         const bool has_tail = (k_bytes % kSliceBytes) != 0;
         int st = gk % ST;                       // stage of slice kt
-        if constexpr (AB == AbType::BF16) {
+        if constexpr (AB == AbType::BF16 || AB == AbType::I8) {
           // Software pipeline over the two 32-deep MFMA steps of a slice.  Step s+1's
           // fragments are read into the other register set while step s's MFMAs
           // issue, and the slice barrier sits between the two steps, so that the
@@ -788,9 +803,14 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_gemm_kernel(GemmArgs args
             if (!live[t]) return;
             const uint4 a = make_uint4(fa[t].x & keep, fa[t].y & keep, fa[t].z & keep, fa[t].w & keep);
 #pragma unroll
-            for (int s = 0; s < SNB; ++s)
-              acc[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fw[s]),
-                                                                  __builtin_bit_cast(bf16x8, a), acc[t][s], 0, 0, 0);
+            for (int s = 0; s < SNB; ++s) {
+              if constexpr (AB == AbType::I8)
+                acc[t][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, fw[s]),
+                                                                  __builtin_bit_cast(i32x4, a), acc[t][s], 0, 0, 0);
+              else
+                acc[t][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fw[s]),
+                                                                    __builtin_bit_cast(bf16x8, a), acc[t][s], 0, 0, 0);
+            }
           };
           // Prologue: the tile's first ST-1 slices.  They are issued after the previous
           // tile's epilogue stores, so waiting for slice 0 needs no wait for those stores
@@ -1131,6 +1151,16 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_gemm_kernel(GemmArgs args
       __syncthreads();
     } else {
     const int cbase = n0 + wn * Cfg::kWNOut + 4 * SNO * g;
+    // 8-bit integers: the scales of the lane's weight rows (columns past N_out repeat its last ones)
+    [[maybe_unused]] f32x4 col_scale[AB == AbType::I8 ? SNB : 1];
+    if constexpr (AB == AbType::I8) {
+      const float* bs = args.b_scales + (long long)e * args.N;
+#pragma unroll
+      for (int s = 0; s < SNB; ++s) {
+        const int half = s / SNO, ss = s - half * SNO;
+        col_scale[s] = *reinterpret_cast<const f32x4*>(bs + half * N_out + min(cbase + 4 * ss, N_out - 4));
+      }
+    }
     // fp8 output: the scale of each row's 128 columns needs the amax over the WN waves
     // that hold them; every row group's partial amax goes through LDS at once, so that
     // a tile's epilogue takes two barriers instead of two per row group
@@ -1163,11 +1193,22 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_gemm_kernel(GemmArgs args
       const bool row_ok = rloc < rows_valid;
       const long long m = (long long)out_row0 + rloc;
       float v[4 * SNO];
+      if constexpr (AB == AbType::I8) {
+        const float sa = row_ok ? args.a_scales[a_row_of((int)m)] : 0.f;
+#pragma unroll
+        for (int s = 0; s < SNO; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = (float)acc[t][s][r] * sa * col_scale[s][r];
+            v[4 * s + r] = SILU ? silu_mul(x, (float)acc[t][SNO + s][r] * sa * col_scale[SNO + s][r]) : x;
+          }
+      } else {
 #pragma unroll
       for (int s = 0; s < SNO; ++s)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           v[4 * s + r] = SILU ? silu_mul(acc[t][s][r], acc[t][SNO + s][r]) : acc[t][s][r];
+      }
 
       if constexpr (CT == CType::FP8) {
         const float scale = fp8_scale[t];
@@ -1432,6 +1473,21 @@ hipError_t launch_grouped_gemm(const GemmLaunch& p, hipStream_t stream) {
     }
     if (p.c_dtype == 1) return launch_cfg<AbType::F32, CType::BF16, false, 64, 64, 2, 2, 1, 2>(a, stream);
     return launch_cfg<AbType::F32, CType::F32, false, 64, 64, 2, 2, 1, 2>(a, stream);
+  }
+  if (p.ab_dtype == 3) {   // 8-bit integers, the tiers of bf16
+    if (p.koff || p.pre_out || p.c_dtype == 2) return hipErrorInvalidValue;
+    auto go = [&](auto silu_tag) {
+      constexpr bool SILU = decltype(silu_tag)::value;
+      if (use_mid_tiles(trows, p.E))
+        return p.c_dtype == 1 ? launch_cfg<AbType::I8, CType::BF16, SILU, MOE_TILE_I8_MID>(a, stream)
+                              : launch_cfg<AbType::I8, CType::F32, SILU, MOE_TILE_I8_MID>(a, stream);
+      if (use_decode_tiles(trows, p.E))
+        return p.c_dtype == 1 ? launch_cfg<AbType::I8, CType::BF16, SILU, MOE_TILE_I8_DEC>(a, stream)
+                              : launch_cfg<AbType::I8, CType::F32, SILU, MOE_TILE_I8_DEC>(a, stream);
+      return p.c_dtype == 1 ? launch_cfg<AbType::I8, CType::BF16, SILU, MOE_TILE_I8>(a, stream)
+                            : launch_cfg<AbType::I8, CType::F32, SILU, MOE_TILE_I8>(a, stream);
+    };
+    return p.silu ? go(std::true_type{}) : go(std::false_type{});
   }
   // fp8 operands
   if (!p.koff && p.c_dtype != 2 && use_decode_tiles(p.M_rows, p.E)) {

@@ -52,7 +52,7 @@ struct GemmLaunch {
   const float* a_scales;
   const void* B;
   const float* b_scales;
-  int ab_dtype;  // moe_dtype_t
+  int ab_dtype;  // moe_dtype_t, or 3: 8-bit integers (a_scales by row of A, b_scales [E, N])
   const int* offsets;
   int E;
   long long M_rows, N, K;
@@ -192,5 +192,35 @@ bool fourbit_fits(long long M_rows, int E, long long N, long long K, bool int4, 
 // n values of whole groups -> codes and scales
 hipError_t launch_quantize_fourbit(const void* w, bool bf16, long long n, bool int4, int group, void* codes,
                                    void* scales, hipStream_t stream);
+
+// rows to 8-bit integers with a scale each (eightbit.hip); H a multiple of 16, up to kNormMaxH
+struct QuantizeLaunch {
+  const void* x;               // [rows, H]
+  bool x_bf16;
+  long long rows;
+  const int* valid;            // device, nullable: only the first *valid rows
+  int H;
+  void* codes;                 // int8 [rows, H]
+  float* scales;               // [rows]
+};
+hipError_t launch_quantize_eightbit(const QuantizeLaunch& p, hipStream_t stream);
+
+// an AdamW step over `count` tensors (adamw.hip)
+struct AdamwLaunch {
+  long long count;
+  void* const* param;          // host arrays
+  const void* const* grad;
+  const int64_t* n;
+  bool p_bf16, g_bf16;
+  bool s8;                     // e4m3 states with scales per 128 elements, else f32
+  void *m, *v;
+  float *m_scale, *v_scale;
+  float* master;               // nullable; with bf16 parameters
+  double lr, beta1, beta2, eps, weight_decay;
+  long long step;
+  const float *schedule, *grad_scale;   // device, nullable
+  const uint64_t* rng;                  // device, nullable
+};
+hipError_t launch_adamw(const AdamwLaunch& p, hipStream_t stream);
 
 }  // namespace moe

@@ -11,12 +11,12 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
 from . import _lib
-from ._lib import MoeAux, load
+from ._lib import MoeAdamw, MoeAux, load
 
 _DT = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16,
        torch.float8_e4m3fn: _lib.MOE_FP8_E4M3}
@@ -441,6 +441,14 @@ def grouped_matvec_fourbit(a: torch.Tensor, codes: torch.Tensor, scales: torch.T
     return out
 
 
+def _new_aux(T: int, E: int, k: int, dev):
+    """Tensors for the routing's results, and the library's struct that names them."""
+    i32 = lambda *shape: torch.empty(*shape, dtype=torch.int32, device=dev)
+    t = ForwardAux(i32(T, k), torch.empty(T, k, dtype=torch.float32, device=dev), i32(E + 1), i32(T * k), i32(T * k))
+    return t, MoeAux(t.topk_ids.data_ptr(), t.topk_weights.data_ptr(), t.offsets.data_ptr(), t.sorted_rows.data_ptr(),
+                     t.row_pos.data_ptr())
+
+
 def forward_fourbit_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
     return load().forward_fourbit_workspace(T, H, I, E, k)
 
@@ -470,15 +478,91 @@ def forward_fourbit(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w1
     if workspace is None:
         workspace = torch.empty(max(lib.forward_fourbit_workspace(T, H, I, E, k), 1), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, device=dev)
-    aux_t = aux_c = None
-    if return_aux:
-        i32 = lambda *shape: torch.empty(*shape, dtype=torch.int32, device=dev)
-        aux_t = ForwardAux(i32(T, k), torch.empty(T, k, dtype=torch.float32, device=dev), i32(E + 1), i32(T * k),
-                           i32(T * k))
-        aux_c = MoeAux(aux_t.topk_ids.data_ptr(), aux_t.topk_weights.data_ptr(), aux_t.offsets.data_ptr(),
-                       aux_t.sorted_rows.data_ptr(), aux_t.row_pos.data_ptr())
+    aux_t, aux_c = _new_aux(T, E, k, dev) if return_aux else (None, None)
     _run(lib.forward_fourbit, dev, _a(x), _a(logits), _a(w13), _a(w13_scale), _a(w2), _a(w2_scale), fmt, group, T, H,
          I, E, k, num_valid_rows, int(bool(renormalize)), _a(out), _DT[out.dtype],
+         ctypes.byref(aux_c) if aux_c is not None else None, _a(workspace), workspace.numel())
+    return (out, aux_t) if return_aux else out
+
+
+def quantize_rows_eightbit(x: torch.Tensor):
+    """x [..., H] (f32 or bf16) -> (int8 codes of x's shape, f32 scales [...]), a scale for each row:
+    of tokens [T, H], or of weights [E, N, K] (a scale for each output channel)."""
+    _need(x, "x", _EL)
+    if x.dim() < 1:
+        raise ValueError("x must have rows")
+    H = x.shape[-1]
+    codes = torch.empty_like(x, dtype=torch.int8)
+    scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    _run(load().quantize_rows_eightbit, x.device, _a(x), _DT[x.dtype], scales.numel(), H, _a(codes), _a(scales))
+    return codes, scales
+
+
+def grouped_gemm_eightbit(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                          offsets: torch.Tensor, epilogue: str = "none", gather_rows: Optional[torch.Tensor] = None,
+                          gather_div: int = 1, out_dtype: Optional[torch.dtype] = None,
+                          out: Optional[torch.Tensor] = None):
+    """grouped_gemm on 8-bit integers: a int8 [A_rows, K] with a_scale f32 [A_rows] x b int8 [E, N, K]
+    with b_scale f32 [E, N] over segments of offsets -> c [M, N or N/2] (bf16 or f32).
+
+    With ``gather_rows`` product row p reads a[gather_rows[p] // gather_div], as in
+    grouped_gemm_gather.
+    """
+    _need(a, "a", torch.int8)
+    dev = a.device
+    A_rows, K = a.shape
+    _need(b, "b", torch.int8, device=dev)
+    E, N, K2 = b.shape
+    if K2 != K:
+        raise ValueError(f"K mismatch: a has {K}, b has {K2}")
+    _need(a_scale, "a_scale", torch.float32, (A_rows,), dev)
+    _need(b_scale, "b_scale", torch.float32, (E, N), dev)
+    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    M = A_rows
+    if gather_rows is not None:
+        _need(gather_rows, "gather_rows", torch.int32, device=dev)
+        M = gather_rows.numel()
+    n_out = N // 2 if epilogue == "silu_mul" else N
+    if out is None:
+        out = a.new_empty(M, n_out, dtype=out_dtype or torch.bfloat16)
+    _need(out, "out", out_dtype or _EL, (M, n_out), dev)
+    _run(load().grouped_gemm_eightbit, dev, _a(a), _a(a_scale), A_rows, _a(gather_rows), int(gather_div), _a(b),
+         _a(b_scale), _a(offsets), E, M, N, K, _EPI[epilogue], _a(out), _DT[out.dtype])
+    return out
+
+
+def forward_eightbit_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
+    return load().forward_eightbit_workspace(T, H, I, E, k)
+
+
+def forward_eightbit(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor,
+                     w2: torch.Tensor, w2_scale: torch.Tensor, k: int, num_valid_rows: int = -1,
+                     renormalize: bool = True, out_dtype: Optional[torch.dtype] = None,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     return_aux: bool = False):
+    """The whole layer on 8-bit integers: x bf16 [T, H], logits f32 [T, E], int8 w13 [E, 2I, H] and
+    w2 [E, H, I] with a scale for each channel, f32 [E, 2I] and [E, H] (quantize_rows_eightbit)
+    -> out [T, H] (bf16 or f32)."""
+    _need(x, "x", torch.bfloat16)
+    T, H = x.shape
+    dev = x.device
+    E, I2, _ = w13.shape
+    I = I2 // 2
+    _need(logits, "logits", torch.float32, (T, E), dev)
+    _need(w13, "w13", torch.int8, (E, 2 * I, H), dev)
+    _need(w13_scale, "w13_scale", torch.float32, (E, 2 * I), dev)
+    _need(w2, "w2", torch.int8, (E, H, I), dev)
+    _need(w2_scale, "w2_scale", torch.float32, (E, H), dev)
+    if out is None:
+        out = torch.empty(T, H, dtype=out_dtype or torch.bfloat16, device=dev)
+    _need(out, "out", out_dtype or _EL, (T, H), dev)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(max(lib.forward_eightbit_workspace(T, H, I, E, k), 1), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, device=dev)
+    aux_t, aux_c = _new_aux(T, E, k, dev) if return_aux else (None, None)
+    _run(lib.forward_eightbit, dev, _a(x), _a(logits), _a(w13), _a(w13_scale), _a(w2), _a(w2_scale), T, H, I, E, k,
+         num_valid_rows, int(bool(renormalize)), _a(out), _DT[out.dtype],
          ctypes.byref(aux_c) if aux_c is not None else None, _a(workspace), workspace.numel())
     return (out, aux_t) if return_aux else out
 
@@ -628,3 +712,108 @@ def unpermute_combine_dropout(y: torch.Tensor, row_pos: torch.Tensor, topk_weigh
          H, k, _a(residual), _lib.MOE_F32 if residual is None else _DT[residual.dtype], p, _a(rng), _a(out),
          _DT[out.dtype])
     return out
+
+
+@dataclass
+class AdamWState:
+    """States of all tensors of adamw_step, one after the other, each from a multiple of 128 elements on.
+
+    float32 m and v, or float8_e4m3fn codes of m and of sqrt(v) with m_scale and v_scale (one
+    float32 for 128 elements); master: the float32 copy of bf16 params, or None.
+    """
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+    master: Optional[torch.Tensor] = None
+
+
+def adamw_starts(params: Sequence[torch.Tensor]):
+    """First element of each tensor in the arrays of AdamWState, and the arrays' elements after the last."""
+    starts, n = [], 0
+    for p in params:
+        starts.append(n)
+        n += (p.numel() + 127) // 128 * 128
+    return starts + [n]
+
+
+def adamw_init(params: Sequence[torch.Tensor], bits: int = 32, master: bool = False) -> AdamWState:
+    """States at the start of a run: zeros, and with ``master`` the params' values in float32."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, not {bits}")
+    if not params:
+        raise ValueError("params is empty")
+    *starts, n = adamw_starts(params)
+    new = lambda size, dtype: params[0].new_zeros(size, dtype=dtype)
+    if bits == 8:
+        code = lambda: new(n, torch.uint8).view(torch.float8_e4m3fn)
+        state = AdamWState(code(), code(), new(n // 128, torch.float32), new(n // 128, torch.float32))
+    else:
+        state = AdamWState(new(n, torch.float32), new(n, torch.float32))
+    if master:
+        state.master = new(n, torch.float32)
+        for p, at in zip(params, starts):
+            state.master[at:at + p.numel()] = p.reshape(-1)
+    return state
+
+
+def adamw_counters(params: Sequence[torch.Tensor]) -> int:
+    """Counters that an adamw_step with rng uses: what to add to rng[1] between calls."""
+    return adamw_starts(params)[-1] // 8
+
+
+def adamw_schedule(lr: float, step: int, betas=(0.9, 0.999)):
+    """What adamw_step's ``schedule`` holds for a learning rate and step."""
+    return lr, 1.0 - betas[0] ** step, 1.0 - betas[1] ** step
+
+
+def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], state: AdamWState, lr: float, step: int,
+               betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+               grad_scale: Optional[torch.Tensor] = None, schedule: Optional[torch.Tensor] = None,
+               rng: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step over all of params, in place (with the states and master).
+
+    params of one dtype and grads of one dtype (f32 or bf16 each), of the same shapes.  ``step``
+    counts from 1.  ``grad_scale``: GPU float32 [1] that multiplies the gradients; infinite or NaN,
+    nothing changes.  ``schedule``: GPU float32 [3] (adamw_schedule's values), in place of lr and
+    step, for a step captured in a graph.  ``rng``: GPU int64 (or uint64) [2], seed and offset: 8-bit
+    states, and bf16 params without master, round by chance in place of to nearest; advance rng[1] by
+    adamw_counters(params) between calls.
+    """
+    count = len(params)
+    if count == 0 or len(grads) != count:
+        raise ValueError(f"{count} params and {len(grads)} grads")
+    dev, p_dtype, g_dtype = params[0].device, params[0].dtype, grads[0].dtype
+    if not params[0].is_cuda or p_dtype not in _EL or g_dtype not in _EL:
+        raise ValueError("params and grads must be GPU tensors of float32 or bfloat16")
+    sizes, total = [], 0
+    for i, (p, g) in enumerate(zip(params, grads)):
+        if p.dtype != p_dtype or g.dtype != g_dtype or p.device != dev or g.device != dev:
+            raise ValueError(f"params[{i}] or grads[{i}] has another dtype or device than the first")
+        if p.shape != g.shape or not p.is_contiguous() or not g.is_contiguous():
+            raise ValueError(f"params[{i}] and grads[{i}] must be contiguous and of one shape")
+        n = p.numel()
+        sizes.append(n)
+        total += (n + 127) // 128 * 128
+    small = state.m.dtype == torch.float8_e4m3fn
+    _need(state.m, "state.m", (torch.float32, torch.float8_e4m3fn), (total,), dev)
+    _need(state.v, "state.v", state.m.dtype, (total,), dev)
+    if small:
+        if state.m_scale is None or state.v_scale is None:
+            raise ValueError("8-bit states need m_scale and v_scale")
+        _need(state.m_scale, "state.m_scale", torch.float32, (total // 128,), dev)
+        _need(state.v_scale, "state.v_scale", torch.float32, (total // 128,), dev)
+    if state.master is not None:
+        _need(state.master, "state.master", torch.float32, (total,), dev)
+    if grad_scale is not None:
+        _need(grad_scale, "grad_scale", torch.float32, (1,), dev)
+    if schedule is not None:
+        _need(schedule, "schedule", torch.float32, (3,), dev)
+    if rng is not None:
+        _need_rng(rng, dev)
+    pointers = ctypes.c_void_p * count
+    _run(load().adamw_step, dev, pointers(*[p.data_ptr() for p in params]), pointers(*[g.data_ptr() for g in grads]),
+         (ctypes.c_int64 * count)(*sizes), count, _DT[p_dtype], _DT[g_dtype], _DT[state.m.dtype], _a(state.m),
+         _a(state.m_scale) if small else None, _a(state.v), _a(state.v_scale) if small else None, _a(state.master),
+         ctypes.byref(MoeAdamw(lr, betas[0], betas[1], eps, weight_decay, step)), _a(schedule), _a(grad_scale),
+         _a(rng))

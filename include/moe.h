@@ -59,7 +59,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 5
+#define MOE_ABI_VERSION 6
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 16
 
@@ -469,6 +469,70 @@ moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, cons
                                  void* stream);
 
 /*
+ * 8-bit integers.  Codes are int8, a value is code * scale with one f32 scale for
+ * each row: of the activations, a token's; of packed weights [E, N, K], an output
+ * channel's ([E, N]).
+ */
+
+/*
+ * moe_quantize_rows_eightbit -- codes and scales of rows, of tokens or of weights
+ * (E*N rows of K):
+ *
+ *   scale = amax / 127,  code = round(x * (127 / amax)) (ties to even)
+ *
+ *   x       [rows, H] of x_dtype (MOE_F32 or MOE_BF16), H a multiple of 16, up to 32768.
+ *   codes   out int8 [rows, H], scales out f32 [rows].
+ *
+ * A row below 2^-100 is zeros with scale 1.  A row with an infinity or NaN gets
+ * an infinite or NaN scale, no other row.
+ */
+moe_status_t moe_quantize_rows_eightbit(const void* x, moe_dtype_t x_dtype, int64_t rows, int64_t H, void* codes,
+                                        float* scales, void* stream);
+
+/*
+ * moe_grouped_gemm_eightbit -- moe_grouped_gemm (gather_rows null) or
+ * moe_grouped_gemm_gather on 8-bit integers:
+ *
+ *   for p in [offsets[e], offsets[e+1]):
+ *       acc[p, n] = a_scales[row(p)] * b_scales[e, n] * sum_k A[row(p), k] * B[e, n, k]
+ *
+ *   A, a_scales  int8 [A_rows, K], f32 [A_rows].  row(p) = p (A_rows >= M_rows), or with
+ *                gather_rows (device int32 [M_rows]) gather_rows[p] / gather_div
+ *                clamped into A.
+ *   B, b_scales  int8 [E, N, K], f32 [E, N].  K a multiple of 16, up to 131056: the
+ *                sums of products are exact 32-bit integers.
+ *   C            [M_rows, N_out] of c_dtype (MOE_F32 or MOE_BF16), rows of whole 16 bytes;
+ *                rows from offsets[E] on are written as exact zeros.
+ *
+ * Everything else (offsets, epi, the 4 GiB limits, errors) is as in moe_grouped_gemm.
+ * With E = 1 it is the plain product.
+ */
+moe_status_t moe_grouped_gemm_eightbit(const void* A, const float* a_scales, int64_t A_rows, const int32_t* gather_rows,
+                                       int32_t gather_div, const void* B, const float* b_scales, const int32_t* offsets,
+                                       int32_t E, int64_t M_rows, int64_t N, int64_t K, moe_epilogue_t epi, void* C,
+                                       moe_dtype_t c_dtype, void* stream);
+
+/* Bytes of device workspace moe_forward_eightbit needs; 0 for sizes that it refuses. */
+size_t moe_forward_eightbit_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k);
+
+/*
+ * moe_forward_eightbit -- moe_forward on 8-bit integers: token rows are quantised
+ * once each (the activation-staging stage), h is rounded to bf16 and quantised by
+ * rows (in the gate/up stage), the expert outputs are rounded to bf16.
+ *
+ *   x            bf16 [T, H]; H and I multiples of 16, up to 32768.
+ *   w13, w2      int8 [E, 2I, H] and [E, H, I]; w13_scales f32 [E, 2I], w2_scales [E, H].
+ *   out          [T, H] of out_dtype (MOE_F32 or MOE_BF16).
+ *
+ * Everything else (aux and its stage events, workspace, errors) is as in moe_forward.
+ */
+moe_status_t moe_forward_eightbit(const void* x, const float* router_logits, const void* w13, const float* w13_scales,
+                                  const void* w2, const float* w2_scales, int64_t T, int64_t H, int64_t I, int32_t E,
+                                  int32_t k, int64_t num_valid_rows, int32_t renormalize, void* out,
+                                  moe_dtype_t out_dtype, moe_aux_t* aux, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
  * moe_layer_norm -- layer norm of token rows (in front of the router and the
  * experts), or its root-mean-square form:
  *
@@ -557,6 +621,69 @@ moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, c
                                            int64_t T, int64_t H, int32_t k, const void* residual,
                                            moe_dtype_t residual_dtype, double p, const uint64_t* rng, void* out,
                                            moe_dtype_t out_dtype, void* stream);
+
+/*
+ * AdamW over many tensors: the step after moe_backward.  With g = grad *
+ * grad_scale, t the number of the step (from 1 on), per element:
+ *
+ *   m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * The tensors' states lie one after the other in arrays of
+ * moe_adamw_state_elements(n, count) elements, each tensor at a multiple of 128
+ * (the elements between are the library's).  f32 states hold m and v.  8-bit
+ * states hold e4m3 codes of m and of sqrt(v), code * scale, with one f32 scale for
+ * 128 consecutive elements of a tensor: scale = amax / 448, codes of
+ * value * (448 / amax); 128 elements below 2^-100 are zeros with scale 1.  A
+ * sqrt(v) above zero has code 1 at least.  All arithmetic is f32, one rounding for
+ * each operation, in the order of the formulas.
+ */
+
+/* Elements of the state arrays of tensors with n[i] elements; -1 for invalid sizes. */
+int64_t moe_adamw_state_elements(const int64_t* n, int64_t count);
+
+typedef struct {
+  double lr;            /* finite, >= 0 */
+  double beta1, beta2;  /* in [0, 1) */
+  double eps;           /* finite, >= 1e-30 */
+  double weight_decay;  /* finite, >= 0 */
+  int64_t step;         /* >= 1 */
+} moe_adamw_t;
+
+/*
+ * moe_adamw_step -- updates params, states and master in place.
+ *
+ *   params, grads  HOST arrays of `count` device pointers, n the HOST array of
+ *                their elements (any number, also 0): p_dtype and g_dtype
+ *                (MOE_F32 or MOE_BF16), 16-byte aligned.  No two params overlap.
+ *                The arrays are read before the call returns.
+ *   state_dtype  MOE_F32 (m_scale, v_scale null) or MOE_FP8_E4M3.
+ *   m, v         states as above, 16-byte aligned; m_scale and v_scale have
+ *                one f32 for 128 elements.  Zeros (scales any finite number) start a run.
+ *   master       f32 copy of bf16 params, laid out like the states (its elements
+ *                between tensors are not touched), nullable: it is what is updated, and
+ *                params become its values rounded to nearest.
+ *   hyper        host values, read before the call returns.
+ *   schedule     device f32 [3], nullable: lr, 1 - beta1^t and 1 - beta2^t, read when
+ *                the kernel runs in place of hyper's lr and step, so that a captured
+ *                graph takes the values that the caller put there.
+ *   grad_scale   device f32 [1], nullable (1): the factor of a norm clip or of an
+ *                unscaled loss.  Infinite or NaN: the call changes nothing.
+ *   rng          device uint64 [2], seed and offset, nullable.  Given, 8-bit codes, and
+ *                bf16 params without master, are rounded up in magnitude with the chance of
+ *                their remainder in place of to nearest: element i of the state
+ *                arrays takes the 16-bit piece i % 8 of Philox4x32-10's counter (low and high word
+ *                of offset + i/8, 2, 0).  A call uses offset + [0, elements/8): advance
+ *                offset by that much between calls.
+ *
+ * A gradient that is infinite or NaN makes its element NaN, with 8-bit states
+ * its 128 elements.  One launch for 64 tensors.
+ */
+moe_status_t moe_adamw_step(void* const* params, const void* const* grads, const int64_t* n, int64_t count,
+                            moe_dtype_t p_dtype, moe_dtype_t g_dtype, moe_dtype_t state_dtype, void* m, float* m_scale,
+                            void* v, float* v_scale, float* master, const moe_adamw_t* hyper, const float* schedule,
+                            const float* grad_scale, const uint64_t* rng, void* stream);
 
 /* Short name of a status code. */
 const char* moe_status_string(moe_status_t status);

@@ -24,8 +24,9 @@ fixes another precision):
                  gradients, by the chain rule through the same per-expert loop.
 
 Around the layer: ``norm.py`` (layer norm and its root-mean-square form, forward and
-backward), ``dropout.py`` (the counter-based generator and dropout with a residual) and
+backward), ``dropout.py`` (the counter-based generator and dropout with a residual),
 ``fourbit.py`` (what 4-bit codes and group scales stand for, and the coding of weights).
+``eightbit.py`` (rows in 8-bit integers and the layer on them) and ``adamw.py`` (an AdamW step).
 
 Sources: the transformers PR #45621 write-up ("MoE 및 FP8 커널 최적화"),
 section 2 (sentinel tokens are excluded from the histogram / sorted as the
@@ -44,4 +45,4 @@ textbook SwiGLU via torch, torch's e4m3 cast, the valid-row counts the
 transformers write-up prints, invariants).  Nothing here is "parity unpinned".
 """
 
-from . import e4m3, routing, layer, gemm, brute, norm, dropout, fourbit  # noqa: F401
+from . import e4m3, routing, layer, gemm, brute, norm, dropout, fourbit, eightbit, adamw  # noqa: F401
