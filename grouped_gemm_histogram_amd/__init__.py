@@ -26,6 +26,8 @@ from .ops import (  # noqa: F401
     dropout_add_backward,
     dropout_counters,
     forward,
+    forward_decode,
+    forward_decode_workspace_bytes,
     forward_eightbit,
     forward_eightbit_workspace_bytes,
     forward_fourbit,

@@ -21,6 +21,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAU
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_EPI_NONE, MOE_EPI_SILU_MUL = 0, 1
 MOE_INT4, MOE_MXFP4 = 0, 1
+MOE_WEIGHTS_BF16, MOE_WEIGHTS_FP8_E4M3, MOE_WEIGHTS_EIGHTBIT, MOE_WEIGHTS_INT4, MOE_WEIGHTS_MXFP4 = range(5)
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -74,6 +75,8 @@ SIGNATURES: dict[str, tuple] = {
     "moe_forward_eightbit_workspace": (SZ, [I64, I64, I64, I32, I32]),
     "moe_forward_eightbit": (I32, [P, P, P, P, P, P, I64, I64, I64, I32, I32, I64, I32, P, I32,
                                    ctypes.POINTER(MoeAux), P, SZ, P]),
+    "moe_forward_decode_workspace": (SZ, [I64, I64, I64, I32, I32]),
+    "moe_forward_decode": (I32, [P, P, P, P, P, P, I32, I32, I64, I64, I64, I32, I32, I64, I32, P, I32, P, SZ, P]),
     "moe_layer_norm": (I32, [P, I32, I64, I64, P, P, I32, F32, I32, P, P, P, P]),
     "moe_layer_norm_backward_workspace": (SZ, [I64, I64]),
     "moe_layer_norm_backward": (I32, [P, P, I32, I64, I64, P, I32, P, P, I32, P, P, P, I32, P, SZ, P]),
@@ -111,6 +114,8 @@ class MoeKernels:
     grouped_gemm_eightbit: Callable
     forward_eightbit_workspace: Callable
     forward_eightbit: Callable
+    forward_decode_workspace: Callable
+    forward_decode: Callable
     layer_norm: Callable
     layer_norm_backward_workspace: Callable
     layer_norm_backward: Callable

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 
+#include "decode_plan.h"
 #include "launch.h"
 #include "moe.h"
 
@@ -1212,6 +1213,88 @@ moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, c
   return launched(moe::launch_combine_dropout(y, y_dtype == MOE_BF16, row_pos, topk_weights, offsets, E, (int)T,
                                               (int)H, k, drop, out, out_dtype == MOE_BF16, as_stream(stream)),
                   "unpermute_combine_dropout");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------- the layer for few tokens
+
+namespace {
+
+moe_status_t check_decode(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, moe_weights_t format, int32_t group) {
+  if (moe_status_t s = check_experts(E, k)) return s;
+  MOE_REQUIRE(T >= 0 && H > 0 && I > 0 && H <= kMaxRows / 2 && I <= kMaxRows / 2, "bad sizes");
+  if (T > moe::kDecodeTokens)
+    return fail(MOE_ERR_UNSUPPORTED, "T=%lld: the layer for few tokens takes up to %d", (long long)T, moe::kDecodeTokens);
+  int unit = 0;
+  switch (format) {
+    case MOE_WEIGHTS_BF16: unit = 8; break;
+    case MOE_WEIGHTS_FP8_E4M3: unit = 128; break;
+    case MOE_WEIGHTS_EIGHTBIT: unit = 16; break;
+    case MOE_WEIGHTS_INT4:
+      MOE_REQUIRE(group == 32 || group == 64 || group == 128, "int4 groups have 32, 64 or 128 channels, not %d", group);
+      unit = group;
+      break;
+    case MOE_WEIGHTS_MXFP4:
+      MOE_REQUIRE(group == 32, "mxfp4 groups have 32 channels, not %d", group);
+      unit = 32;
+      break;
+    default: return fail(MOE_ERR_INVALID_ARG, "bad format %d", (int)format);
+  }
+  MOE_REQUIRE(H % unit == 0 && I % unit == 0, "H=%lld and I=%lld must be multiples of %d", (long long)H, (long long)I,
+              unit);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+  if (check_decode(T, H, I, E, k, MOE_WEIGHTS_BF16, 0)) return 0;
+  return align256(moe::decode_plan_bytes()) + align256(T * k * I * 2);
+}
+
+moe_status_t moe_forward_decode(const void* x, const float* router_logits, const void* w13, const void* w13_scales,
+                                const void* w2, const void* w2_scales, moe_weights_t format, int32_t group, int64_t T,
+                                int64_t H, int64_t I, int32_t E, int32_t k, int64_t num_valid_rows, int32_t renormalize,
+                                void* out, moe_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (moe_status_t s = check_decode(T, H, I, E, k, format, group)) return s;
+  MOE_REQUIRE(f32_or_bf16(out_dtype), "out_dtype must be MOE_F32 or MOE_BF16");
+  const bool scaled = format != MOE_WEIGHTS_BF16;
+  if (T > 0) {
+    MOE_REQUIRE(x && router_logits && w13 && w2 && out && (!scaled || (w13_scales && w2_scales)), "null pointer argument");
+    MOE_REQUIRE(aligned16(x) && aligned16(w13) && aligned16(w2) && aligned16(out) &&
+                    (!scaled || (aligned16(w13_scales) && aligned16(w2_scales))),
+                "x, weights, scales and out must be 16-byte aligned");
+  }
+  const size_t plan = align256(moe::decode_plan_bytes()), need = plan + align256(T * k * I * 2);
+  if (!workspace || workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  MOE_REQUIRE(aligned16(workspace), "workspace must be 16-byte aligned");
+  if (T == 0) return ok();
+  const long long R = T * k;
+  moe::DecodeLaunch p{};
+  p.x = x;
+  p.logits = router_logits;
+  p.w13 = w13;
+  p.w13_scales = w13_scales;
+  p.w2 = w2;
+  p.w2_scales = w2_scales;
+  p.format = format;
+  p.group = group;
+  p.T = (int)T;
+  p.H = (int)H;
+  p.I = (int)I;
+  p.E = E;
+  p.k = k;
+  p.valid = (int)(num_valid_rows >= 0 && num_valid_rows < R ? num_valid_rows : R);
+  p.renorm = renormalize != 0;
+  p.plan = workspace;
+  p.h = static_cast<uint8_t*>(workspace) + plan;
+  p.out = out;
+  p.out_bf16 = out_dtype == MOE_BF16;
+  return launched(moe::launch_decode(p, as_stream(stream)), "forward_decode");
 }
 
 }  // extern "C"

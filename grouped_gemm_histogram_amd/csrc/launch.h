@@ -205,6 +205,23 @@ struct QuantizeLaunch {
 };
 hipError_t launch_quantize_eightbit(const QuantizeLaunch& p, hipStream_t stream);
 
+// the layer for up to 16 tokens (decode.hip); format: moe_weights_t
+struct DecodeLaunch {
+  const void* x;               // bf16 [T, H]
+  const float* logits;         // [T, E]
+  const void *w13, *w13_scales, *w2, *w2_scales;
+  int format, group;
+  int T, H, I, E, k;
+  int valid;                   // flat rows that are routed, in [0, T k]
+  bool renorm;
+  void* plan;                  // decode_plan_bytes()
+  void* h;                     // bf16 [T k, I]
+  void* out;                   // [T, H]
+  bool out_bf16;
+};
+size_t decode_plan_bytes();
+hipError_t launch_decode(const DecodeLaunch& p, hipStream_t stream);
+
 // an AdamW step over `count` tensors (adamw.hip)
 struct AdamwLaunch {
   long long count;

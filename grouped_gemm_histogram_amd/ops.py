@@ -567,6 +567,65 @@ def forward_eightbit(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w
     return (out, aux_t) if return_aux else out
 
 
+def forward_decode_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
+    return load().forward_decode_workspace(T, H, I, E, k)
+
+
+def forward_decode(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, k: int,
+                   num_valid_rows: int = -1, renormalize: bool = True, w13_scale: Optional[torch.Tensor] = None,
+                   w2_scale: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The whole layer for up to 16 tokens, in two kernels: x bf16 [T, H], logits f32 [T, E] -> out [T, H]
+    (bf16 or f32).
+
+    w13 [E, 2I, H] and w2 [E, H, I] are bf16, e4m3 with block scales (as in forward), int8 with
+    channel scales (as in forward_eightbit), or uint8 4-bit codes [E, 2I, H/2] and [E, H, I/2]
+    with their scales (as in forward_fourbit).  Activations are not quantised.
+    """
+    _need(x, "x", torch.bfloat16)
+    T, H = x.shape
+    dev = x.device
+    _need(w13, "w13", (torch.bfloat16, torch.float8_e4m3fn, torch.int8, torch.uint8), device=dev)
+    group = 0
+    if w13.dtype == torch.uint8:
+        if w13_scale is None or w2_scale is None:
+            raise ValueError("4-bit weights need w13_scale and w2_scale")
+        E, I2, H2, fmt, group = _fourbit(w13, w13_scale, dev, "w13 ")
+        E2, Hn, I, fmt2, group2 = _fourbit(w2, w2_scale, dev, "w2 ")
+        if (E2, Hn, 2 * I, H2) != (E, H, I2, H):
+            raise ValueError(f"w13 [{E}, {I2}, {H2}] and w2 [{E2}, {Hn}, {I}] do not fit x [{T}, {H}]")
+        if (fmt, group) != (fmt2, group2):
+            raise ValueError("w13 and w2 must have one format and group")
+        fmt = _lib.MOE_WEIGHTS_MXFP4 if fmt == _lib.MOE_MXFP4 else _lib.MOE_WEIGHTS_INT4
+    else:
+        E, I2, _ = w13.shape
+        I = I2 // 2
+        _need(w13, "w13", None, (E, 2 * I, H), dev)
+        _need(w2, "w2", w13.dtype, (E, H, I), dev)
+        if w13.dtype == torch.bfloat16:
+            fmt = _lib.MOE_WEIGHTS_BF16
+            if w13_scale is not None or w2_scale is not None:
+                raise ValueError("bf16 weights have no scales")
+        else:
+            if w13_scale is None or w2_scale is None:
+                raise ValueError("8-bit weights need w13_scale and w2_scale")
+            fp8 = w13.dtype == torch.float8_e4m3fn
+            fmt = _lib.MOE_WEIGHTS_FP8_E4M3 if fp8 else _lib.MOE_WEIGHTS_EIGHTBIT
+            _need(w13_scale, "w13_scale", torch.float32, (E, 2 * I // 128, H // 128) if fp8 else (E, 2 * I), dev)
+            _need(w2_scale, "w2_scale", torch.float32, (E, H // 128, I // 128) if fp8 else (E, H), dev)
+    _need(logits, "logits", torch.float32, (T, E), dev)
+    if out is None:
+        out = x.new_empty(T, H, dtype=out_dtype or torch.bfloat16)
+    _need(out, "out", out_dtype or _EL, (T, H), dev)
+    lib = load()
+    if workspace is None:
+        workspace = x.new_empty(max(lib.forward_decode_workspace(T, H, I, E, k), 1), dtype=torch.uint8)
+    _need(workspace, "workspace", torch.uint8, device=dev)
+    _run(lib.forward_decode, dev, _a(x), _a(logits), _a(w13), _a(w13_scale), _a(w2), _a(w2_scale), fmt, group, T, H, I,
+         E, k, num_valid_rows, int(bool(renormalize)), _a(out), _DT[out.dtype], _a(workspace), workspace.numel())
+    return out
+
+
 @dataclass
 class NormStats:
     mean: Optional[torch.Tensor]  # f32 [T]; None in the root-mean-square form

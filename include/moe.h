@@ -77,6 +77,14 @@ typedef enum { MOE_EPI_NONE = 0, MOE_EPI_SILU_MUL = 1 } moe_epilogue_t;
 
 typedef enum { MOE_INT4 = 0, MOE_MXFP4 = 1 } moe_fourbit_t;
 
+typedef enum {
+  MOE_WEIGHTS_BF16 = 0,
+  MOE_WEIGHTS_FP8_E4M3 = 1,
+  MOE_WEIGHTS_EIGHTBIT = 2,
+  MOE_WEIGHTS_INT4 = 3,
+  MOE_WEIGHTS_MXFP4 = 4
+} moe_weights_t;
+
 /*
  * moe_route_topk -- the router's choice of a small subset of experts per
  * token ([MoEs], MoE basics).
@@ -531,6 +539,41 @@ moe_status_t moe_forward_eightbit(const void* x, const float* router_logits, con
                                   int32_t k, int64_t num_valid_rows, int32_t renormalize, void* out,
                                   moe_dtype_t out_dtype, moe_aux_t* aux, void* workspace, size_t workspace_bytes,
                                   void* stream);
+
+/* Bytes of device workspace moe_forward_decode needs (for every format); 0 for
+ * invalid sizes or T > 16. */
+size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k);
+
+/*
+ * moe_forward_decode -- the whole layer for up to 16 tokens in two kernels: the
+ * routing of moe_route_topk, h = silu(W13_gate x) * (W13_up x) and out = sum of the
+ * weighted W2 h, in place of moe_forward's, moe_forward_eightbit's and
+ * moe_forward_fourbit's five and more.
+ *
+ *   x            bf16 [T, H], T up to 16 (more is MOE_ERR_UNSUPPORTED).
+ *   w13, w2      [E, 2I, H] and [E, H, I] in `format`, with their scales:
+ *                MOE_WEIGHTS_BF16      none; H and I multiples of 8
+ *                MOE_WEIGHTS_FP8_E4M3  f32 for each 128 x 128 block, as in moe_forward;
+ *                                      multiples of 128
+ *                MOE_WEIGHTS_EIGHTBIT  f32 [E, 2I] and [E, H] (moe_quantize_rows_eightbit);
+ *                                      multiples of 16
+ *                MOE_WEIGHTS_INT4, MOE_WEIGHTS_MXFP4
+ *                                      codes and scales of moe_quantize_fourbit with
+ *                                      `group`; multiples of 32 and of group
+ *   router_logits, num_valid_rows, renormalize: as for moe_route_topk.
+ *   out          [T, H] of out_dtype (MOE_F32 or MOE_BF16); tokens without a valid row
+ *                get exact zeros.
+ *   workspace    >= moe_forward_decode_workspace(...) bytes; no initialisation needed.
+ *
+ * Activations are not quantised in any format: x is taken as it is and h rounded to
+ * bf16; products accumulate in f32, expert outputs are not rounded, out is rounded
+ * once.  int4 sums code * x over 32 channels before their scale and takes 8 * x off, so
+ * 15 * sum |x| of them, and 23 * |scale| times it summed over K, have to stay in f32's range.
+ */
+moe_status_t moe_forward_decode(const void* x, const float* router_logits, const void* w13, const void* w13_scales,
+                                const void* w2, const void* w2_scales, moe_weights_t format, int32_t group, int64_t T,
+                                int64_t H, int64_t I, int32_t E, int32_t k, int64_t num_valid_rows, int32_t renormalize,
+                                void* out, moe_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * moe_layer_norm -- layer norm of token rows (in front of the router and the
