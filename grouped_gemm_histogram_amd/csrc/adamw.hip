@@ -81,7 +81,7 @@ __device__ __forceinline__ uint32_t e4m3_by_chance(float x, uint32_t piece) {
   return min(code, 126u) | ((__float_as_uint(x) >> 24) & 0x80u);
 }
 
-// 8 codes of a block of 128 elements (16 lanes): scale = amax / 448.  kLeast: values above zero keep code 1.
+// 8 codes of a block of 128 elements (16 lanes): scale = amax * (1 / 448).  kLeast: values above zero keep code 1.
 template <bool kLeast>
 __device__ __forceinline__ uint2 pack_block(const float (&x)[kPer], const uint4& bits, bool chance, float& scale) {
 #pragma clang fp contract(off)
@@ -99,9 +99,9 @@ __device__ __forceinline__ uint2 pack_block(const float (&x)[kPer], const uint4&
   amax = fmaxf(amax, rotated(amax, std::integral_constant<int, 4>{}));
   amax = fmaxf(amax, rotated(amax, std::integral_constant<int, 2>{}));
   amax = fmaxf(amax, rotated(amax, std::integral_constant<int, 1>{}));
-  const bool some = amax >= 0x1p-100f;   // below: zeros (448 / amax is finite above)
-  scale = some ? amax / 448.0f : 1.0f;
-  const float inv = some ? 448.0f / amax : 0.0f;
+  const bool some = amax >= 0x1p-100f;   // below: zeros (1 / amax is finite above)
+  scale = some ? amax * (1.0f / 448.0f) : 1.0f;
+  const float inv = some ? 448.0f * (1.0f / amax) : 0.0f;
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < kPer; j += 2) {

@@ -41,7 +41,7 @@ struct FmtOf {
   static constexpr int kVal = 128 / kBits;            // weights in 16 bytes
   static constexpr int kX = kVal / 8;                 // 16-byte pieces of activations for them
   static constexpr int kGroup = F == kInt4x32 || F == kMxfp4 ? 32 : F == kInt4x64 ? 64 : 128;
-  // bytes of a weight row in a step: four lanes' 16, once or twice
+  // 64-byte pieces of a weight row in a step: four lanes' 16 bytes, once or twice
   static constexpr int kPieces = kFour ? 1 : 2;
   static constexpr int kStep = 64 * kPieces;
   static constexpr int kGroups = kInt4 ? std::max(1, 64 * 2 / kGroup) : 1;   // int4 scales of a step
@@ -53,12 +53,14 @@ struct Step {
   using T = FmtOf<F>;
   uint4 w[NM][T::kPieces];
   uint4 x[T::kPieces][T::kX];
-  float s[NM][T::kGroups];   // int4: scales; mxfp4: the piece's e8m0 byte, as an integer's bits
+  uint32_t s[NM][T::kGroups];   // bits of int4's f32 scales or e4m3's block scale, or mxfp4's byte
 };
 
-__device__ __forceinline__ uint4 keep_if(uint4 v, bool keep) {
-  const uint32_t m = keep ? 0xffffffffu : 0u;
-  return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
+// 16 bytes, or zeros
+__device__ __forceinline__ uint4 load_if(bool live, const uint8_t* p) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (live) v = *reinterpret_cast<const uint4*>(p);
+  return v;
 }
 
 // four signed bytes as bf16
@@ -79,66 +81,69 @@ __device__ __forceinline__ bf16x8 unpack8(uint32_t lo, uint32_t hi) {   // 8 cod
   return as_bf16x8(make_uint4(a.x, a.y, b.x, b.y));
 }
 
-// NM weight rows' products with an expert's tokens over the steps first, first + stride, ... of their K.
+// NM weight rows' products with an expert's tokens over the steps of a wave: units of 128 bytes of
+// the rows, first, first + stride, ...
 //
-// MFMA layout: the lane's weight row is column lane % 16 of the result, the lane's token row (xrow) row
+// MFMA layout: the lane's weight row is column lane % 16 of the result, the lane's token row row
 // lane % 16 of the activations; lane / 16 = g picks the lane's 16 bytes of a 64-byte piece.  acc[m][r]
 // becomes the sum of token 4 g + r and the lane's weight row.  int4: after a transpose of
 // words between the lane groups each MFMA has 32 consecutive channels, so activations are read to fit that.
+//
+// Addresses are a scalar base that walks along the row and a 32-bit offset of the lane that stays: three
+// vector registers for all streams.
 template <int F, int NM, int DEPTH>
 struct Products {
   using T = FmtOf<F>;
-  const uint8_t* w[NM];      // the lane's weight rows
-  const uint8_t* x;          // the lane's token row
-  const uint8_t* s[NM];      // scales: the lane's rows' (int4, mxfp4) or of the 16 rows' blocks (e4m3)
+  const uint8_t* w[NM];      // uniform: the expert's first weight row
+  uint32_t w_off;            // the lane's row, and 16 g
+  const uint8_t* x;          // uniform
+  uint32_t x_off;            // the lane's token row, and its channels of a piece
+  const uint8_t* s[NM];      // uniform
+  uint32_t s_off;            // int4, mxfp4: the lane's row (mxfp4: and g)
   int row_bytes;             // of a weight row
-  int groups;                // scales of a row
   int g;
 
-  // steps come in units of 128 bytes of a row, `stride` units apart
-  __device__ __forceinline__ int byte_of(int first, int stride, int i) const {
-    if constexpr (T::kPieces == 2) return (first + i * stride) * 128;
-    return (first + (i >> 1) * stride) * 128 + (i & 1) * 64;
-  }
+  static __device__ __forceinline__ uint32_t x_lane(int g) { return T::kInt4 ? 16 * g : 16 * T::kX * g; }
 
+  template <bool WHOLE>
   __device__ __forceinline__ void load(Step<F, NM>& b, int at) const {
-    const int last = row_bytes - 16;
+    const uint8_t* xs = x + (long long)(at / 16) * (T::kVal * 2);
 #pragma unroll
     for (int p = 0; p < T::kPieces; ++p) {
-      const int o = at + 64 * p + 16 * g;
+      const bool live = WHOLE || at + 64 * p + 16 * g < row_bytes;
 #pragma unroll
       for (int q = 0; q < T::kX; ++q) {
-        // int4: the lane's 8 channels of 32-channel piece q; else the q-th 8 of its own piece
-        const int k0 = T::kInt4 ? (at + 16 * q) * 2 + 8 * g : o / 16 * T::kVal + 8 * q;
-        const int k_last = row_bytes / 16 * T::kVal - 8;
-        b.x[p][q] = *reinterpret_cast<const uint4*>(x + 2 * min(k0, k_last));
+        // int4: the lane's 8 channels of the q-th 32; else the q-th 8 of its own piece's
+        const uint8_t* from = xs + (T::kInt4 ? 64 * q : 64 * T::kX * p + 16 * q);
+        b.x[p][q] = load_if(T::kInt4 ? WHOLE || at + 16 * q < row_bytes : live, from + x_off);
       }
 #pragma unroll
-      for (int m = 0; m < NM; ++m) b.w[m][p] = *reinterpret_cast<const uint4*>(w[m] + min(o, last));
-    }
-    if constexpr (F == kMxfp4) {
-#pragma unroll
-      for (int m = 0; m < NM; ++m) b.s[m][0] = __uint_as_float(s[m][min(at / 16 + g, groups - 1)]);
-    }
-    if constexpr (T::kInt4) {
-      const int first = at * 2 / T::kGroup;
-#pragma unroll
       for (int m = 0; m < NM; ++m)
+        b.w[m][p] = load_if(live, w[m] + at + 64 * p + w_off);
+    }
 #pragma unroll
-        for (int q = 0; q < T::kGroups; ++q)
-          b.s[m][q] = reinterpret_cast<const float*>(s[m])[min(first + q, groups - 1)];
+    for (int m = 0; m < NM; ++m) {
+      if constexpr (F == kE4m3) b.s[m][0] = *reinterpret_cast<const uint32_t*>(s[m] + (at >> 7) * 4);
+      if constexpr (F == kMxfp4) {
+        b.s[m][0] = 0;
+        if (WHOLE || at + 16 * g < row_bytes) b.s[m][0] = *(s[m] + (at >> 4) + s_off);
+      }
+      if constexpr (T::kInt4) {
+        const uint8_t* from = s[m] + at * 2 / T::kGroup * 4;
+        if constexpr (WHOLE) {
+          __builtin_memcpy(b.s[m], from + s_off, 4 * T::kGroups);
+        } else {
+#pragma unroll
+          for (int q = 0; q < T::kGroups; ++q) {
+            b.s[m][q] = 0;
+            if (at + q * (T::kGroup / 2) < row_bytes) __builtin_memcpy(&b.s[m][q], from + 4 * q + s_off, 4);
+          }
+        }
+      }
     }
   }
 
-  __device__ __forceinline__ void use(Step<F, NM>& b, int at, const float (&block)[NM], f32x4 (&acc)[NM]) const {
-    // channels past the row hold copies of its last ones: their activations are zeroed
-    if (at + T::kStep > row_bytes) {
-#pragma unroll
-      for (int p = 0; p < T::kPieces; ++p)
-#pragma unroll
-        for (int q = 0; q < T::kX; ++q)
-          b.x[p][q] = keep_if(b.x[p][q], T::kInt4 ? at + 16 * q < row_bytes : at + 64 * p + 16 * g < row_bytes);
-    }
+  static __device__ __forceinline__ void use(const Step<F, NM>& b, f32x4 (&acc)[NM]) {
     if constexpr (F == kBf16) {
 #pragma unroll
       for (int p = 0; p < T::kPieces; ++p)
@@ -160,16 +165,16 @@ struct Products {
 #pragma unroll
       for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[m][r] = F == kE4m3 ? fmaf(part[m][r], block[m], acc[m][r]) : part[m][r];
+        for (int r = 0; r < 4; ++r)
+          acc[m][r] = F == kE4m3 ? fmaf(part[m][r], __uint_as_float(b.s[m][0]), acc[m][r]) : part[m][r];
     } else if constexpr (F == kMxfp4) {
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         const uint4 v = b.w[m][0];
         const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t e8m0 = __float_as_uint(b.s[m][0]);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b.x[0][q]), as_bf16x8(unpack_mxfp4(d[q], e8m0)),
+          acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b.x[0][q]), as_bf16x8(unpack_mxfp4(d[q], b.s[m][0])),
                                                            acc[m], 0, 0, 0);
       }
     } else {
@@ -200,46 +205,83 @@ struct Products {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(part[m][r], b.s[m][q0 / kPer], acc[m][r]);
+          for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(part[m][r], __uint_as_float(b.s[m][q0 / kPer]), acc[m][r]);
       }
     }
   }
 
-  // first, stride: in units of 128 bytes
-  __device__ __forceinline__ void run(int first, int stride, f32x4 (&acc)[NM]) const {
+  // steps of a share: units first, first + stride, ... of a row
+  static __device__ __forceinline__ int steps(int row_bytes, int first, int stride) {
     const int units = (row_bytes + 127) >> 7;
-    int n = first < units ? (units - first + stride - 1) / stride : 0;   // this wave's units
-    if constexpr (T::kPieces == 1) n *= 2;
-    Step<F, NM> b[DEPTH];
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i)
-      if (i < n) load(b[i], byte_of(first, stride, i));
-    for (int i0 = 0; i0 < n; i0 += DEPTH) {
-#pragma unroll
-      for (int j = 0; j < DEPTH; ++j) {
-        const int i = i0 + j;
-        if (i < n) {
-          const int at = byte_of(first, stride, i);
-          float block[NM];
-#pragma unroll
-          for (int m = 0; m < NM; ++m)
-            block[m] = F == kE4m3 ? reinterpret_cast<const float*>(s[m])[min(at >> 7, groups - 1)] : 1.0f;
-          use(b[j], at, block, acc);
-          if (i + DEPTH < n) load(b[j], byte_of(first, stride, i + DEPTH));
-        }
-      }
-    }
+    const int n = first < units ? (units - first + stride - 1) / stride : 0;
+    if constexpr (T::kPieces == 2) return n;
+    const bool half = n > 0 && first + (n - 1) * stride == units - 1 && row_bytes <= units * 128 - 64;
+    return 2 * n - (half ? 1 : 0);
   }
 };
 
+// Streams the products of jobs 0 to jobs - 1 through a wave: the loads run DEPTH steps ahead of the MFMAs, across the
+// ends of jobs.  start(job, products, first, stride) sets a job's streams and its share of K, steps_of(job)
+// is the number of its steps (at least one), finish(job, sums) takes its sums.
+template <int F, int NM, int DEPTH, typename Start, typename Steps, typename Finish>
+__device__ __forceinline__ void stream(int jobs, Start&& start, Steps&& steps_of, Finish&& finish) {
+  using P = Products<F, NM, DEPTH>;
+  using T = FmtOf<F>;
+  if (jobs <= 0) return;
+  P p;
+  int first = 0, stride = 1, load_job = 0, load_step = 0;
+  start(0, p, first, stride);
+  int load_steps = steps_of(0);
+  int use_job = 0, left = load_steps;   // of the job in use
+  auto get = [&](Step<F, NM>& b) {
+    if (load_job >= jobs) return;
+    const int at = T::kPieces == 2 ? (first + load_step * stride) * 128
+                                   : (first + (load_step >> 1) * stride) * 128 + (load_step & 1) * 64;
+    if (at + T::kStep <= p.row_bytes)
+      p.template load<true>(b, at);
+    else
+      p.template load<false>(b, at);
+    if (++load_step == load_steps) {
+      load_step = 0;
+      if (++load_job < jobs) {
+        start(load_job, p, first, stride);
+        load_steps = steps_of(load_job);
+      }
+    }
+  };
+  Step<F, NM> b[DEPTH];
+  f32x4 acc[NM];
+#pragma unroll
+  for (int m = 0; m < NM; ++m) acc[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < DEPTH; ++j) get(b[j]);
+  while (true) {
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) {
+      P::use(b[j], acc);
+      get(b[j]);
+      if (--left == 0) {
+        finish(use_job, acc);
+        if (++use_job == jobs) return;
+        left = steps_of(use_job);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) acc[m] = f32x4{0, 0, 0, 0};
+      }
+    }
+  }
+}
+
 template <int F>
-constexpr int kDepthUp = FmtOf<F>::kInt4 ? 2 : 3;
+constexpr int kDepthUp = FmtOf<F>::kInt4 || F == kE4m3 ? 2 : 3;
 template <int F>
-constexpr int kDepthDown = FmtOf<F>::kInt4 ? 3 : 4;
+constexpr int kDepthDown = FmtOf<F>::kInt4 || F == kE4m3 ? 3 : 4;
+// workgroups on a CU that the registers leave room for
+template <int F>
+constexpr int kUpGroups = F == kInt4x32 ? 3 : 4;
 
 constexpr int kUpWaves = 4;
 constexpr int kDownWaves = 8;
-constexpr int kDownParts = 512;   // routed rows times shares of K that the second kernel's LDS holds
+constexpr int kDownParts = 768;   // routed rows times shares of K that the second kernel's LDS holds
 
 struct UpArgs {
   const uint8_t* x;       // [T, H] bf16
@@ -252,13 +294,30 @@ struct UpArgs {
   uint16_t* h;            // [T k, I] bf16
 };
 
-// bytes of `group`-channel scales of a weight row, or of a row of blocks
+// bytes of the scales of a weight row of K channels (e4m3: of a row of blocks)
 template <int F>
-__device__ __forceinline__ const uint8_t* scales_at(const uint8_t* s, long long row, int K) {
-  if constexpr (F == kE4m3) return s + (row >> 7) * (K / 128) * 4;
-  if constexpr (F == kMxfp4) return s + row * (K / 32);
-  if constexpr (FmtOf<F>::kInt4) return s + row * (K / FmtOf<F>::kGroup) * 4;
-  return s;
+__device__ __forceinline__ int scale_bytes(int K) {
+  if constexpr (F == kE4m3) return K / 128 * 4;
+  if constexpr (F == kMxfp4) return K / 32;
+  if constexpr (FmtOf<F>::kInt4) return K / FmtOf<F>::kGroup * 4;
+  return 0;
+}
+
+// the streams of a wave whose lanes' weight rows are base + n, n below 2^32 bytes of weights on
+template <int F, int NM, int DEPTH>
+__device__ __forceinline__ void set_rows(Products<F, NM, DEPTH>& p, const uint8_t* w, const uint8_t* s,
+                                         const long long (&base)[NM], int n0, int n, int K) {
+  const int g = lane_id() >> 4, sb = scale_bytes<F>(K);
+  p.g = g;
+  p.row_bytes = K / FmtOf<F>::kVal * 16;
+  p.w_off = (uint32_t)n * (uint32_t)p.row_bytes + 16 * g;
+  p.s_off = (uint32_t)n * (uint32_t)sb + (F == kMxfp4 ? g : 0);
+#pragma unroll
+  for (int m = 0; m < NM; ++m) {
+    p.w[m] = w + base[m] * p.row_bytes;
+    // e4m3: the block row of columns n0 to n0 + 15
+    p.s[m] = F == kE4m3 ? s + ((base[m] + n0) >> 7) * sb : s + base[m] * sb;
+  }
 }
 
 // Routes the tokens and lists the experts that have rows, in the order of their first row, with their
@@ -303,7 +362,7 @@ __device__ __forceinline__ void make_plan(const UpArgs& a, DecodePlan& plan, uin
 }
 
 template <int F, int EPL>
-__global__ __launch_bounds__(kUpWaves * kWave, 4) void decode_up_kernel(UpArgs a) {
+__global__ __launch_bounds__(kUpWaves * kWave, kUpGroups<F>) void decode_up_kernel(UpArgs a) {
   using T = FmtOf<F>;
   __shared__ DecodePlan plan;
   __shared__ uint32_t tokens[EPL * kWave], index[EPL * kWave];
@@ -316,25 +375,20 @@ __global__ __launch_bounds__(kUpWaves * kWave, 4) void decode_up_kernel(UpArgs a
       reinterpret_cast<uint4*>(a.plan)[i] = from[i];
   }
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int items = plan.active * a.blocks;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int at = item / a.blocks, n0 = (item - at * a.blocks) * 16;
-    const int e = plan.expert[at], count = plan.count[at];
-    Products<F, 2, kDepthUp<F>> p;
-    p.row_bytes = a.H / T::kVal * 16;
-    p.groups = a.H / T::kGroup;
-    p.g = lane >> 4;
-    const int n = min(n0 + (lane & 15), a.I - 1);   // columns past I repeat the last one
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const long long row = (long long)e * 2 * a.I + m * a.I + n;
-      p.w[m] = a.w + row * p.row_bytes;
-      p.s[m] = scales_at<F>(a.s, row, a.H);
-    }
-    const int mine = plan.rows[at][min(lane & 15, count - 1)];   // tokens past the expert's repeat its last
-    p.x = a.x + (long long)(mine / a.k) * a.H * 2;
-    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-    p.run(wave, kUpWaves, acc);
+  const int active = __builtin_amdgcn_readfirstlane(plan.active);
+  const int items = active * a.blocks;   // (expert, 16 columns): blockIdx.x, + gridDim.x, ...
+  const int jobs = items > (int)blockIdx.x ? (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  auto item_of = [&](int job, int& at, int& n0) {
+    const int item = (int)blockIdx.x + job * (int)gridDim.x;
+    at = item / a.blocks;
+    n0 = (item - at * a.blocks) * 16;
+  };
+  const int steps = Products<F, 2, 1>::steps(a.H / T::kVal * 16, wave, kUpWaves);
+  // the waves' sums of an item: joined by every thread for one token and column
+  auto finish = [&](int job, const f32x4 (&acc)[2]) {
+    int at, n0;
+    item_of(job, at, n0);
+    const int count = plan.count[at];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -348,12 +402,33 @@ __global__ __launch_bounds__(kUpWaves * kWave, 4) void decode_up_kernel(UpArgs a
         v[m] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kUpWaves; ++i) v[m] += part[i][m][j][threadIdx.x & 15];
-        if (F == kInt8) v[m] *= reinterpret_cast<const float*>(a.s)[(long long)e * 2 * a.I + m * a.I + c];
+        if (F == kInt8)
+          v[m] *= reinterpret_cast<const float*>(a.s)[(long long)plan.expert[at] * 2 * a.I + m * a.I + c];
       }
       a.h[(long long)plan.rows[at][j] * a.I + c] = f32_to_bf16_bits(silu_mul(v[0], v[1]));
     }
     __syncthreads();
+  };
+  if (steps == 0) {   // a row of fewer units than waves: nothing to add
+    const f32x4 none[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+    for (int job = 0; job < jobs; ++job) finish(job, none);
+    return;
   }
+  stream<F, 2, kDepthUp<F>>(
+      jobs,
+      [&](int job, auto& p, int& first, int& stride) {
+        int at, n0;
+        item_of(job, at, n0);
+        const int e = __builtin_amdgcn_readfirstlane(plan.expert[at]), count = plan.count[at];
+        const long long row = (long long)e * 2 * a.I;
+        // columns past I repeat the last one, tokens past the expert's its last
+        set_rows(p, a.w, a.s, {row, row + a.I}, n0, min(n0 + (lane & 15), a.I - 1), a.H);
+        p.x = a.x;
+        p.x_off = (uint32_t)(plan.rows[at][min(lane & 15, count - 1)] / a.k) * (uint32_t)a.H * 2 + p.x_lane(p.g);
+        first = wave;
+        stride = kUpWaves;
+      },
+      [&](int) { return steps; }, finish);
 }
 
 struct DownArgs {
@@ -376,31 +451,39 @@ __global__ __launch_bounds__(kDownWaves * kWave, 4) void decode_down_kernel(Down
   __syncthreads();
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16, n = min(n0 + (lane & 15), a.H - 1);
-  const int active = plan.active;
-  // Shares of K: about two units of work a wave.  shares * valid <= kDownParts: an active expert has up to 16 of
-  // the valid rows, and shares * active <= 16 + active - 1 while active < 16; from there on there is one
-  // share of up to 256 rows.
-  const int shares = active ? (2 * kDownWaves + active - 1) / active : 1;
-  for (int unit = wave; unit < active * shares; unit += kDownWaves) {
-    const int at = unit / shares, share = unit - at * shares;
-    const int e = plan.expert[at], count = plan.count[at];
-    Products<F, 1, kDepthDown<F>> p;
-    p.row_bytes = a.I / T::kVal * 16;
-    p.groups = a.I / T::kGroup;
-    p.g = lane >> 4;
-    const long long row = (long long)e * a.H + n;
-    p.w[0] = a.w + row * p.row_bytes;
-    p.s[0] = scales_at<F>(a.s, row, a.I);
-    p.x = reinterpret_cast<const uint8_t*>(a.h + (long long)plan.rows[at][min(lane & 15, count - 1)] * a.I);
-    f32x4 acc[1] = {f32x4{0, 0, 0, 0}};
-    p.run(share, shares, acc);
-    const float scale = F == kInt8 ? reinterpret_cast<const float*>(a.s)[row] : 1.0f;
+  const int active = __builtin_amdgcn_readfirstlane(plan.active);
+  // Shares of K: about four jobs a wave, at least one unit each.  shares * valid <= kDownParts: an active
+  // expert has up to 16 of the valid rows, so while active < 16 it is at most 16 * (32 + active - 1), up to
+  // 31 two shares of 256 rows, then one.
+  const int row_bytes = a.I / T::kVal * 16;
+  const int shares = active ? min((4 * kDownWaves + active - 1) / active, (row_bytes + 127) >> 7) : 1;
+  const int units = active * shares;
+  stream<F, 1, kDepthDown<F>>(
+      units > wave ? (units - wave + kDownWaves - 1) / kDownWaves : 0,
+      [&](int job, auto& p, int& first, int& stride) {
+        const int unit = wave + job * kDownWaves, at = unit / shares;
+        const int e = __builtin_amdgcn_readfirstlane(plan.expert[at]), count = plan.count[at];
+        set_rows(p, a.w, a.s, {(long long)e * a.H}, n0, n, a.I);
+        p.x = reinterpret_cast<const uint8_t*>(a.h);
+        p.x_off = (uint32_t)plan.rows[at][min(lane & 15, count - 1)] * (uint32_t)a.I * 2 + p.x_lane(p.g);
+        first = unit - at * shares;
+        stride = shares;
+      },
+      [&](int job) {
+        const int unit = wave + job * kDownWaves;
+        return Products<F, 1, 1>::steps(row_bytes, unit - unit / shares * shares, shares);
+      },
+      [&](int job, const f32x4 (&acc)[1]) {
+        const int unit = wave + job * kDownWaves, at = unit / shares, share = unit - at * shares;
+        const int count = plan.count[at];
+        float scale = 1.0f;
+        if (F == kInt8) scale = reinterpret_cast<const float*>(a.s)[(long long)plan.expert[at] * a.H + n];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = 4 * (lane >> 4) + r;
-      if (j < count) part[share * a.valid + plan.rows[at][j]][lane & 15] = F == kInt8 ? acc[0][r] * scale : acc[0][r];
-    }
-  }
+        for (int r = 0; r < 4; ++r) {
+          const int j = 4 * (lane >> 4) + r;
+          if (j < count) part[share * a.valid + plan.rows[at][j]][lane & 15] = F == kInt8 ? acc[0][r] * scale : acc[0][r];
+        }
+      });
   __syncthreads();
   const int t = threadIdx.x >> 4, c = n0 + (threadIdx.x & 15);
   if (t >= a.T || c >= a.H) return;
@@ -421,9 +504,9 @@ __global__ __launch_bounds__(kDownWaves * kWave, 4) void decode_down_kernel(Down
 
 template <int F, int EPL>
 hipError_t launch_up(const UpArgs& a, hipStream_t stream) {
-  // four workgroups on each of 256 CUs; an expert's columns in workgroups of their own while they last
+  // what fits on 256 CUs at once
   const long long items = (long long)std::min(a.valid, a.E) * a.blocks;
-  const int grid = (int)std::max(1ll, std::min<long long>(items, 256 * 4));
+  const int grid = (int)std::max(1ll, std::min<long long>(items, 256 * kUpGroups<F>));
   hipLaunchKernelGGL((decode_up_kernel<F, EPL>), dim3(grid), dim3(kUpWaves * kWave), 0, stream, a);
   return hipGetLastError();
 }

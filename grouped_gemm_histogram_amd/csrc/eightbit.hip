@@ -1,7 +1,7 @@
 // eightbit.hip -- rows to 8-bit integers with a scale each: token rows in front of the 8-bit grouped
 // product (gemm.hip), and weight rows, whose scale is then the output channel's.
 //
-//     scale = amax / 127,   code = round(x * (127 / amax)), ties to even
+//     scale = amax * (1 / 127),   code = round(x * (127 * (1 / amax))), ties to even, each operation in f32
 //
 // A row stays in the registers of 1 to 16 waves between its largest value and its codes, so x is read
 // once: 3 bytes an element of bf16.  The maximum is taken on the values' bits without their
@@ -80,9 +80,9 @@ __global__ __launch_bounds__(kQuantWaves<W> * 64) void quantize_rows_kernel(cons
   }
   if (!live) return;
   const float amax = __uint_as_float(top);
-  const bool none = amax < 0x1p-100f;   // a row of zeros: 127 / amax is finite for all others
-  const float scale = none ? 1.0f : amax / 127.0f;
-  const float inv = none ? 0.0f : 127.0f / amax;
+  const bool none = amax < 0x1p-100f;   // a row of zeros: 1 / amax is finite for all others
+  const float scale = none ? 1.0f : amax * (1.0f / 127.0f);
+  const float inv = none ? 0.0f : 127.0f * (1.0f / amax);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * W * kWave + rl) * EL;

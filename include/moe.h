@@ -486,7 +486,8 @@ moe_status_t moe_forward_fourbit(const void* x, const float* router_logits, cons
  * moe_quantize_rows_eightbit -- codes and scales of rows, of tokens or of weights
  * (E*N rows of K):
  *
- *   scale = amax / 127,  code = round(x * (127 / amax)) (ties to even)
+ *   scale = amax * (1/127),  code = round(x * (127 * (1/amax))) (ties to even),
+ *   each operation rounded to f32
  *
  *   x       [rows, H] of x_dtype (MOE_F32 or MOE_BF16), H a multiple of 16, up to 32768.
  *   codes   out int8 [rows, H], scales out f32 [rows].
@@ -677,8 +678,8 @@ moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, c
  * moe_adamw_state_elements(n, count) elements, each tensor at a multiple of 128
  * (the elements between are the library's).  f32 states hold m and v.  8-bit
  * states hold e4m3 codes of m and of sqrt(v), code * scale, with one f32 scale for
- * 128 consecutive elements of a tensor: scale = amax / 448, codes of
- * value * (448 / amax); 128 elements below 2^-100 are zeros with scale 1.  A
+ * 128 consecutive elements of a tensor: scale = amax * (1/448), codes of
+ * value * (448 * (1/amax)); 128 elements below 2^-100 are zeros with scale 1.  A
  * sqrt(v) above zero has code 1 at least.  All arithmetic is f32, one rounding for
  * each operation, in the order of the formulas.
  */

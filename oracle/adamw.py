@@ -55,7 +55,7 @@ def code_block(x, piece, least_one: bool):
     amax = np.abs(x).max()
     if amax < F(2.0 ** -100):
         return np.zeros(x.shape, np.uint8), F(1.0)
-    scale, inv = F(amax / F(448.0)), F(F(448.0) / amax)
+    scale, inv = F(amax * (F(1.0) / F(448.0))), F(F(448.0) * (F(1.0) / amax))
     q = (x * inv).astype(F)
     if piece is None:
         code = e4m3.encode(q)

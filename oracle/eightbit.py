@@ -19,8 +19,9 @@ def quantize_rows(x):
     amax = np.abs(x).max(axis=-1)
     none = amax < TINY
     safe = np.where(none, np.float32(1.0), amax)
-    scale = np.where(none, np.float32(1.0), safe / np.float32(127.0)).astype(np.float32)
-    inv = np.where(none, np.float32(0.0), np.float32(127.0) / safe).astype(np.float32)
+    one = np.float32(1.0)
+    scale = np.where(none, one, safe * (one / np.float32(127.0))).astype(np.float32)
+    inv = np.where(none, np.float32(0.0), np.float32(127.0) * (one / safe)).astype(np.float32)
     return np.rint(x * inv[..., None]).astype(np.int8), scale
 
 

@@ -36,7 +36,7 @@ def test_quantize_rows(rows, H, dtype):
     say("quantize", rows, H, dtype)
     rng = np.random.default_rng(rows * H)
     x = torch.from_numpy((rng.normal(size=(rows, H)) * np.exp(rng.normal(size=(rows, 1)))).astype(np.float32)).to(dtype)
-    x[0, H // 2] = 2 * x[0].abs().max()                          # its half is a tie
+    x[0, H // 2] = 2 * x[0].abs().max()                          # its half is next to a tie
     x[0, 1] = x[0, H // 2] / 2
     if rows > 2:
         x[1] = 0
