@@ -1243,6 +1243,13 @@ moe_status_t check_decode(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
   }
   MOE_REQUIRE(H % unit == 0 && I % unit == 0, "H=%lld and I=%lld must be multiples of %d", (long long)H, (long long)I,
               unit);
+  if ((format == MOE_WEIGHTS_INT4 || format == MOE_WEIGHTS_MXFP4) && (H < 128 || I < 128))
+    return fail(MOE_ERR_UNSUPPORTED, "H=%lld, I=%lld: the layer for few tokens takes 4-bit rows of at least 128 channels",
+                (long long)H, (long long)I);
+  const long long e_w = format == MOE_WEIGHTS_BF16 ? 4 : format == MOE_WEIGHTS_INT4 || format == MOE_WEIGHTS_MXFP4 ? 1 : 2;
+  MOE_REQUIRE(I * H <= (long long)UINT32_MAX / e_w, "one expert's W13 must span under 4 GiB");
+  MOE_REQUIRE(T * H * 2 <= (long long)INT32_MAX && T * k * I * 2 <= (long long)INT32_MAX,
+              "x and the hidden rows must each span under 2 GiB");
   return MOE_OK;
 }
 

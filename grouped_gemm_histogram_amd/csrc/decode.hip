@@ -8,24 +8,31 @@
 // operands in registers, where all of these codes are exact, and scales multiply f32 sums (mxfp4's
 // powers of two the operand).
 //
-// The bytes of the routed experts' weights bound it: every weight is read once, straight into registers, a
-// few 128-byte pieces of 16 weight rows ahead in each wave.  The 16 tokens' side of
-// v_mfma_f32_16x16x32_bf16 takes an expert's tokens, as many as there are: one token costs what 16 do.
-// Activations come from the caches in the same order as the weights, so that the wait for
-// a piece's weights is the wait for its activations too.
+// The bytes of the routed experts' weights bound it: every weight is read once, in whole cache lines of 8 rows a load.
+// One v_mfma_f32_16x16x32_bf16 has 8 rows of each of two experts and up to 8 tokens of each: of its 16 x 16
+// results the two 8 x 8 blocks where expert and token belong together are used.  So a wave works on 8 columns at
+// a time, which splits the columns of small layers over more workgroups; an expert of more than 8
+// tokens is listed twice.
 //
 // The routing is recomputed by each workgroup of the first kernel (a wave a token at a time; a third launch or
-// a wait between workgroups would cost more) and left for the second one.  In the first a
-// workgroup's four waves share K of 16 columns (16 gate and 16 up rows) of one expert; in the second eight
-// waves share all experts' K of 16 output columns, so that a token's sum over its experts ends in one place
-// and needs no atomics: sums are joined through LDS in a fixed order.
+// a wait between workgroups would cost more) and left for the second one.  In the first kernel 1, 2, 4 or 8 waves share
+// K of 8 columns of two experts; in the second eight waves share all experts' K of 8 output columns, so
+// that a token's sum over its experts ends in one place and needs no atomics: sums are joined through LDS in a
+// fixed order.
+//
+// First and second kernel, and the bytes of the weights that they read: bf16, 1 token, 4 experts of 2880 x 2880: 25.4
+// and 15.6 us, 133 and 66 MB (5.2 and 4.2 TB/s); e4m3, 8 tokens, 27 experts of 7168 x 2048: 138 and 91 us, about 790 and
+// 395 MB (5.7 and 4.3); mxfp4, 4 tokens, 15 experts of 2880 x 2880: 38 and 25.5 us, about 132 and 66 MB (3.5 and 2.6:
+// rows of 1440 bytes, so that each 128 bytes are parts of two cache lines; with activations, scales and products
+// left out 33 and 18 us); int4 with groups of 32, 16 tokens, 68 experts of 2048 x 768: 45 and 25 us, about 134 and
+// 67 MB (3.0 and 2.7; 8 and 3 steps a row).
 
 #include <algorithm>
+#include <type_traits>
 
 #include "decode_plan.h"
 #include "fourbit_device.h"
 #include "launch.h"
-#include "route_device.h"
 
 namespace moe {
 
@@ -39,28 +46,39 @@ struct FmtOf {
   static constexpr bool kFour = kInt4 || F == kMxfp4;
   static constexpr int kBits = F == kBf16 ? 16 : kFour ? 4 : 8;
   static constexpr int kVal = 128 / kBits;            // weights in 16 bytes
-  static constexpr int kX = kVal / 8;                 // 16-byte pieces of activations for them
+  static constexpr int kX = kVal / 8;                 // MFMAs of a 64-byte piece
+  static constexpr int kXBytes = kVal * 2;            // activations of 16 bytes of weights
   static constexpr int kGroup = F == kInt4x32 || F == kMxfp4 ? 32 : F == kInt4x64 ? 64 : 128;
-  // 64-byte pieces of a weight row in a step: four lanes' 16 bytes, once or twice
-  static constexpr int kPieces = kFour ? 1 : 2;
-  static constexpr int kStep = 64 * kPieces;
-  static constexpr int kGroups = kInt4 ? std::max(1, 64 * 2 / kGroup) : 1;   // int4 scales of a step
+  static constexpr int kGroups = kInt4 ? 128 / kGroup : 1;   // int4 scales of a piece
+  static constexpr int kScale = kInt4 ? 4 * kGroups : F == kBf16 || F == kInt8 ? 0 : 4;   // bytes that a lane loads
+  static constexpr int kXRow = 8 * kXBytes;           // bytes of a token's activations in a step
+  static constexpr int kXTokens = 512 / kXRow;        // tokens of each of two experts that a load of 1 KB holds
 };
 
-// one step's weights, activations and scales of a lane
-template <int F, int NM>
+// bytes of a weight row in a step: a cache line, two pieces of four lanes' 16 bytes
+constexpr int kStep = 128;
+
+// One step's weights, scales and activations of a lane.  NX: loads of activations, which hold kXTokens * NX tokens of each
+// expert; NX = 8 (4 bits only): of all eight tokens, in the MFMA's layout.
+template <int F, int NM, int NX>
 struct Step {
   using T = FmtOf<F>;
-  uint4 w[NM][T::kPieces];
-  uint4 x[T::kPieces][T::kX];
-  uint32_t s[NM][T::kGroups];   // bits of int4's f32 scales or e4m3's block scale, or mxfp4's byte
+  uint4 w[NM][2];
+  uint4 x[NX];
+  uint32_t s[T::kGroups];   // bits of int4's f32 scales or e4m3's block scale, or mxfp4's four bytes
+  int left;                 // uniform: bytes of the row from the step on
 };
 
-// 16 bytes, or zeros
-__device__ __forceinline__ uint4 load_if(bool live, const uint8_t* p) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (live) v = *reinterpret_cast<const uint4*>(p);
-  return v;
+// A buffer load's offset that is past the end of any buffer here: the lane gets zeros and no memory is read.
+constexpr uint32_t kPast = 0x80000000u;
+
+__device__ __forceinline__ auto buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+
+template <int AUX = 0>   // 2: nontemporal
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t rows, uint32_t lane_offset, int offset) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rows, (int)lane_offset, offset, AUX));
 }
 
 // four signed bytes as bf16
@@ -81,207 +99,330 @@ __device__ __forceinline__ bf16x8 unpack8(uint32_t lo, uint32_t hi) {   // 8 cod
   return as_bf16x8(make_uint4(a.x, a.y, b.x, b.y));
 }
 
-// NM weight rows' products with an expert's tokens over the steps of a wave: units of 128 bytes of
-// the rows, first, first + stride, ...
+// Eight weight rows of each of two experts (NM times) times up to eight tokens of each, over a wave's steps of 128 bytes
+// of the rows: first, first + stride, ...
 //
-// MFMA layout: the lane's weight row is column lane % 16 of the result, the lane's token row row
-// lane % 16 of the activations; lane / 16 = g picks the lane's 16 bytes of a 64-byte piece.  acc[m][r]
-// becomes the sum of token 4 g + r and the lane's weight row.  int4: after a transpose of
-// words between the lane groups each MFMA has 32 consecutive channels, so activations are read to fit that.
+// MFMA layout: the lane's weight row, of the first expert for c = lane % 16 < 8, else of the second, is column c of the
+// result, the lane's token row (of the same expert) row c of the activations; g = lane / 16 picks the lane's 16 bytes
+// of a 64-byte piece.  acc[m][r] becomes the sum of token row 4 g + r and weight row c, one of an expert and its own token
+// where g / 2 = c / 8.
 //
-// Addresses are a scalar base that walks along the row and a 32-bit offset of the lane that stays: three
-// vector registers for all streams.
-template <int F, int NM, int DEPTH>
+// Loads take whole cache lines in the lanes' order: 8 lanes a weight row's 128 bytes, one load for each expert's rows;
+// activations of as many tokens as the largest expert has.  They go to the MFMA's layout through LDS of the wave.  (A
+// load of weights in that layout, 16 rows for 16 lanes in a row, took the first-level cache 37 accesses where lines in
+// order take 8; of activations, with every expert's eight tokens, eight loads for mxfp4's two of weights: the second
+// kernel took 34 us with them and 23 without.)
+//
+// A lane loads the scales of one weight row, matrix and 64-byte piece, and all four lanes of a row find
+// theirs in LDS (loaded by each lane for itself they took a fifth of mxfp4's time).
+//
+// A lane's 16 bytes are 16 or 32 channels of the narrower formats, several MFMAs' share.  Words change places between
+// the lane groups (8 bits: halves, 2 swaps; 4 bits: a 4 x 4 transpose), so that each MFMA has 32
+// consecutive channels and 4-bit groups have one scale in an MFMA.
+//
+// Addresses are a buffer's base, a scalar offset that walks along the row and 32-bit offsets of the lane that stay.
+template <int F, int NM, int NX>
 struct Products {
   using T = FmtOf<F>;
-  const uint8_t* w[NM];      // uniform: the expert's first weight row
-  uint32_t w_off;            // the lane's row, and 16 g
-  const uint8_t* x;          // uniform
-  uint32_t x_off;            // the lane's token row, and its channels of a piece
-  const uint8_t* s[NM];      // uniform
-  uint32_t s_off;            // int4, mxfp4: the lane's row (mxfp4: and g)
-  int row_bytes;             // of a weight row
-  int g;
+  using S = Step<F, NM, NX>;
+  static constexpr bool kDirect = NX == 8;
+  // LDS of a wave: weights, activations, scales
+  static constexpr int kW = NM * 2048, kX = kDirect ? 0 : NX * 1024, kLds = kW + kX + 64 * T::kScale;
+  const uint8_t* w[NM][2];    // uniform: the two experts' first weight rows
+  uint32_t w_bytes;           // of an expert's rows of a matrix, below kPast
+  uint32_t w_off;             // the loads' row and byte
+  const uint8_t* x;           // uniform
+  uint32_t x_bytes;           // below kPast
+  uint32_t x_off[kDirect ? 1 : NX];   // the loads' rows and bytes; kPast where an expert has no such token
+  const uint8_t* s;           // the scales that the lane loads: of its row, matrix and piece
+  int row_bytes;              // of a weight row
 
-  static __device__ __forceinline__ uint32_t x_lane(int g) { return T::kInt4 ? 16 * g : 16 * T::kX * g; }
+  // byte of the lane's 8 channels of an MFMA's 32: 8 bits in the order that the swap of halves leaves
+  static __device__ __forceinline__ int x_lane() {
+    const int g = lane_id() >> 4;
+    return T::kBits == 8 ? 32 * (g & 1) + 8 * (g & 2) : 16 * g;
+  }
+  // the bytes of a step that the lane loads of its weight row and of its token row
+  static __device__ __forceinline__ int w_lane() { return 16 * (lane_id() & 7); }
+  static __device__ __forceinline__ int x_load() { return 16 * lane_id() & (T::kXRow - 1); }
+  // load i's token in lanes of this lane's place, and which of the two experts' it is
+  static __device__ __forceinline__ int x_row(int i) { return i * 2 * T::kXTokens + lane_id() / (T::kXRow / 16); }
+  // the lane's scales: of matrix m, piece p
+  static __device__ __forceinline__ int s_matrix() { return NM == 2 ? lane_id() >> 5 : 0; }
+  static __device__ __forceinline__ int s_piece() { return F == kE4m3 ? 0 : (lane_id() >> 4) & 1; }
 
-  template <bool WHOLE>
-  __device__ __forceinline__ void load(Step<F, NM>& b, int at) const {
-    const uint8_t* xs = x + (long long)(at / 16) * (T::kVal * 2);
+  // 4 bits: scales in a 64-byte piece
+  static constexpr int kPieceGroups = 128 / T::kGroup;
+
+  // One set of loads for every step.  Of a row's last, shorter one lanes past its end load zeros (scales: the row's
+  // last ones, which end_row() brings into place), and so does each lane with `past` = kPast, past the last step of all.
+  __device__ __forceinline__ void load(S& b, int at, uint32_t past) const {
+    const int left = row_bytes - at;
+    b.left = left;
+    const int x_left = left / 16 * T::kXBytes;
+    const uint32_t wo = w_off | past | (w_lane() < left ? 0u : kPast);
+    const auto rows = buffer(x, x_bytes);
+    const int x_at = at / 16 * T::kXBytes;
+    if constexpr (kDirect) {
 #pragma unroll
-    for (int p = 0; p < T::kPieces; ++p) {
-      const bool live = WHOLE || at + 64 * p + 16 * g < row_bytes;
+      for (int i = 0; i < 2 * T::kX; ++i)
+        b.x[i] = load16(rows, (x_off[0] | past | (64 * i + x_lane() < x_left ? 0u : kPast)) + 64 * i, x_at);
+    } else {
+      const uint32_t end = past | (x_load() < x_left ? 0u : kPast);
 #pragma unroll
-      for (int q = 0; q < T::kX; ++q) {
-        // int4: the lane's 8 channels of the q-th 32; else the q-th 8 of its own piece's
-        const uint8_t* from = xs + (T::kInt4 ? 64 * q : 64 * T::kX * p + 16 * q);
-        b.x[p][q] = load_if(T::kInt4 ? WHOLE || at + 16 * q < row_bytes : live, from + x_off);
-      }
-#pragma unroll
-      for (int m = 0; m < NM; ++m)
-        b.w[m][p] = load_if(live, w[m] + at + 64 * p + w_off);
+      for (int i = 0; i < NX; ++i)
+        b.x[i] = load16(rows, x_off[i] | end, x_at);
     }
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      if constexpr (F == kE4m3) b.s[m][0] = *reinterpret_cast<const uint32_t*>(s[m] + (at >> 7) * 4);
-      if constexpr (F == kMxfp4) {
-        b.s[m][0] = 0;
-        if (WHOLE || at + 16 * g < row_bytes) b.s[m][0] = *(s[m] + (at >> 4) + s_off);
-      }
-      if constexpr (T::kInt4) {
-        const uint8_t* from = s[m] + at * 2 / T::kGroup * 4;
-        if constexpr (WHOLE) {
-          __builtin_memcpy(b.s[m], from + s_off, 4 * T::kGroups);
-        } else {
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
-          for (int q = 0; q < T::kGroups; ++q) {
-            b.s[m][q] = 0;
-            if (at + q * (T::kGroup / 2) < row_bytes) __builtin_memcpy(&b.s[m][q], from + 4 * q + s_off, 4);
-          }
-        }
+      for (int p = 0; p < 2; ++p)   // read once: not kept in the caches
+        b.w[m][p] = load16<2>(buffer(w[m][p], w_bytes), wo, at);
+    if constexpr (F == kE4m3) b.s[0] = *reinterpret_cast<const uint32_t*>(s + (at >> 7) * 4);
+    if constexpr (T::kFour) {
+      // the piece's first scale; rows have at least 128 channels
+      const int group = min((at + 64 * s_piece()) * 2 / T::kGroup, row_bytes * 2 / T::kGroup - kPieceGroups);
+      __builtin_memcpy(b.s, s + group * (F == kMxfp4 ? 1 : 4), T::kScale);
+    }
+  }
+
+  // Of a row's last, shorter step: brings 4-bit scales, which were the row's last ones, into place.
+  static __device__ __forceinline__ void end_row(S& b) {
+    if constexpr (T::kFour) {
+      // scales of the piece that the row lacks; a piece past the row has no activations left
+      const int by = max(kPieceGroups - max(b.left - 64 * s_piece(), 0) * 2 / T::kGroup, 0) & (kPieceGroups - 1);
+      if constexpr (F == kMxfp4) {
+        b.s[0] >>= 8 * by;
+      } else {
+#pragma unroll
+        for (int bit = 1; bit < T::kGroups; bit *= 2)
+#pragma unroll
+          for (int q = 0; q + bit < T::kGroups; ++q) b.s[q] = by & bit ? b.s[q + bit] : b.s[q];
       }
     }
   }
 
-  static __device__ __forceinline__ void use(const Step<F, NM>& b, f32x4 (&acc)[NM]) {
-    if constexpr (F == kBf16) {
+  // Loaded lines to LDS, and from there in the MFMA's layout.  16-byte chunk j of weight row r is kept at j ^ (r % 8),
+  // of a token's row at j ^ (token + 8 * expert), within 128 bytes where a row has no more: neither side has bank conflicts.
+  static __device__ __forceinline__ int x_chunk(int row, int chunk) {
+    return T::kXRow * row + 16 * (chunk ^ (T::kXRow == 128 ? row >> 1 & 7 : (row >> 1 & 7) | (row & 1) << 3));
+  }
+  static __device__ __forceinline__ void put(uint8_t* lds, const S& b) {
+    const int lane = lane_id(), r = lane >> 3;
 #pragma unroll
-      for (int p = 0; p < T::kPieces; ++p)
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint4*>(lds + 2048 * m + 1024 * i + 128 * r + 16 * ((lane & 7) ^ r)) = b.w[m][i];
+    if constexpr (!kDirect) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) *reinterpret_cast<uint4*>(lds + kW + x_chunk(x_row(i), x_load() / 16)) = b.x[i];
+    }
+    if constexpr (T::kScale > 0) {
+      uint32_t* to = reinterpret_cast<uint32_t*>(lds + kW + kX + T::kScale * (4 * (lane & 15) + (lane >> 4)));
+#pragma unroll
+      for (int i = 0; i < T::kGroups; ++i) to[i] = b.s[i];
+    }
+  }
+  static __device__ __forceinline__ void get_weights(const uint8_t* lds, int m, int p, uint32_t (&d)[4]) {
+    const int c = lane_id() & 15, g = lane_id() >> 4;
+    const uint4 v = *reinterpret_cast<const uint4*>(lds + 2048 * m + 128 * c + 16 * ((4 * p + g) ^ (c & 7)));
+    d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+  }
+  // the activations of the step's MFMA i; tokens past the loaded ones repeat the last
+  static __device__ __forceinline__ bf16x8 get_x(const uint8_t* lds, const S& b, int i) {
+    if constexpr (kDirect) {
+      return as_bf16x8(b.x[i]);
+    } else {
+      const int c = lane_id() & 15, row = 2 * min(c & 7, T::kXTokens * NX - 1) + (c >> 3);
+      return as_bf16x8(*reinterpret_cast<const uint4*>(lds + kW + x_chunk(row, 4 * i + x_lane() / 16)));
+    }
+  }
+  static __device__ __forceinline__ void get_scales(const uint8_t* lds, int m, int p, uint32_t (&d)[T::kGroups]) {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(lds + kW + kX + T::kScale * (4 * (lane_id() & 15) + 2 * m + p));
+#pragma unroll
+    for (int i = 0; i < T::kGroups; ++i) d[i] = from[i];
+  }
+
+  static __device__ __forceinline__ void use(uint8_t* lds, const S& b, f32x4 (&acc)[NM]) {
+    f32x4 part[NM];   // e4m3: the block's sum
+#pragma unroll
+    for (int m = 0; m < NM; ++m) part[m] = f32x4{0, 0, 0, 0};
+    put(lds, b);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (T::kFour) __builtin_amdgcn_sched_barrier(0);   // one piece's operands at a time
+      uint32_t d[NM][4], s[NM][T::kGroups];
+#pragma unroll
+      for (int m = 0; m < NM; ++m) get_weights(lds, m, p, d[m]);
+      bf16x8 x[T::kX];
+#pragma unroll
+      for (int q = 0; q < T::kX; ++q) x[q] = get_x(lds, b, T::kX * p + q);
+      if constexpr (T::kFour) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) get_scales(lds, m, p, s[m]);
+      }
+      if constexpr (F == kBf16) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
-          acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b.x[p][0]), as_bf16x8(b.w[m][p]), acc[m], 0, 0, 0);
-    } else if constexpr (F == kInt8 || F == kE4m3) {
-      f32x4 part[NM];
-#pragma unroll
-      for (int m = 0; m < NM; ++m) part[m] = F == kE4m3 ? f32x4{0, 0, 0, 0} : acc[m];
-#pragma unroll
-      for (int p = 0; p < T::kPieces; ++p)
+          acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              x[0], as_bf16x8(make_uint4(d[m][0], d[m][1], d[m][2], d[m][3])), acc[m], 0, 0, 0);
+      } else if constexpr (F == kInt8 || F == kE4m3) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-          const uint4 v = b.w[m][p];
-          part[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b.x[p][0]), unpack8<F>(v.x, v.y), part[m], 0, 0, 0);
-          part[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b.x[p][1]), unpack8<F>(v.z, v.w), part[m], 0, 0, 0);
+          // rows 2, 3 of the first half change places with rows 0, 1 of the second
+          const auto lo = __builtin_amdgcn_permlane32_swap(d[m][0], d[m][2], false, false);
+          const auto hi = __builtin_amdgcn_permlane32_swap(d[m][1], d[m][3], false, false);
+          f32x4& sum = F == kE4m3 ? part[m] : acc[m];
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], unpack8<F>(lo[0], hi[0]), sum, 0, 0, 0);
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], unpack8<F>(lo[1], hi[1]), sum, 0, 0, 0);
         }
+      } else if constexpr (F == kMxfp4) {
 #pragma unroll
-      for (int m = 0; m < NM; ++m)
+        for (int m = 0; m < NM; ++m) {
+          transpose4(d[m]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[m][r] = F == kE4m3 ? fmaf(part[m][r], __uint_as_float(b.s[m][0]), acc[m][r]) : part[m][r];
-    } else if constexpr (F == kMxfp4) {
+          for (int q = 0; q < 4; ++q)
+            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                x[q], as_bf16x8(unpack_mxfp4(d[m][q], s[m][0] >> (8 * q) & 0xffu)), acc[m], 0, 0, 0);
+        }
+      } else {
 #pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const uint4 v = b.w[m][0];
-        const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+        for (int m = 0; m < NM; ++m) transpose4(d[m]);
+        // a group's sum of code * x starts from -8 * sum of x
+        const bf16x8 minus8 = as_bf16x8(make_uint4(0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u));
+        constexpr int kPer = 4 / T::kGroups;   // MFMAs of a scale
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b.x[0][q]), as_bf16x8(unpack_mxfp4(d[q], b.s[m][0])),
-                                                           acc[m], 0, 0, 0);
-      }
-    } else {
-      uint32_t d[NM][4];
+        for (int q0 = 0; q0 < 4; q0 += kPer) {
+          f32x4 group[NM];
 #pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const uint4 v = b.w[m][0];
-        d[m][0] = v.x, d[m][1] = v.y, d[m][2] = v.z, d[m][3] = v.w;
-        transpose4(d[m]);
-      }
-      // a group's sum of code * x starts from -8 * sum of x
-      const bf16x8 minus8 = as_bf16x8(make_uint4(0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u));
-      constexpr int kPer = 4 / T::kGroups;   // MFMAs of a scale
+          for (int q = q0; q < q0 + kPer; ++q) {
+            const f32x4 start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], minus8, f32x4{0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
-      for (int q0 = 0; q0 < 4; q0 += kPer) {
-        f32x4 part[NM];
+            for (int m = 0; m < NM; ++m) {
+              const f32x4 one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  x[q], as_bf16x8(unpack_int4_ordered(d[m][q])), start, 0, 0, 0);
 #pragma unroll
-        for (int q = q0; q < q0 + kPer; ++q) {
-          const bf16x8 xo = as_bf16x8(order_int4(b.x[0][q]));
-          const f32x4 start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, minus8, f32x4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-          for (int m = 0; m < NM; ++m) {
-            const f32x4 one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, as_bf16x8(unpack_int4(d[m][q])), start, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) part[m][r] = q == q0 ? one[r] : part[m][r] + one[r];
+              for (int r = 0; r < 4; ++r) group[m][r] = q == q0 ? one[r] : group[m][r] + one[r];
+            }
           }
+#pragma unroll
+          for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(group[m][r], __uint_as_float(s[m][q0 / kPer]), acc[m][r]);
+          // here and now: moved behind the branches that follow, the step's 16 products stay in registers until then
+#pragma unroll
+          for (int m = 0; m < NM; ++m) asm volatile("" : "+v"(acc[m]));
         }
+      }
+    }
+    if constexpr (F == kE4m3) {
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+      for (int m = 0; m < NM; ++m) {
+        uint32_t s[1];
+        get_scales(lds, m, 0, s);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(part[m][r], __uint_as_float(b.s[m][q0 / kPer]), acc[m][r]);
+        for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(part[m][r], __uint_as_float(s[0]), acc[m][r]);
       }
     }
   }
 
-  // steps of a share: units first, first + stride, ... of a row
+  // steps of a share of a row
   static __device__ __forceinline__ int steps(int row_bytes, int first, int stride) {
-    const int units = (row_bytes + 127) >> 7;
-    const int n = first < units ? (units - first + stride - 1) / stride : 0;
-    if constexpr (T::kPieces == 2) return n;
-    const bool half = n > 0 && first + (n - 1) * stride == units - 1 && row_bytes <= units * 128 - 64;
-    return 2 * n - (half ? 1 : 0);
+    const int units = (row_bytes + kStep - 1) / kStep;
+    return first < units ? (units - first + stride - 1) / stride : 0;
   }
 };
 
-// Streams the products of jobs 0 to jobs - 1 through a wave: the loads run DEPTH steps ahead of the MFMAs, across the
-// ends of jobs.  start(job, products, first, stride) sets a job's streams and its share of K, steps_of(job)
-// is the number of its steps (at least one), finish(job, sums) takes its sums.
-template <int F, int NM, int DEPTH, typename Start, typename Steps, typename Finish>
-__device__ __forceinline__ void stream(int jobs, Start&& start, Steps&& steps_of, Finish&& finish) {
-  using P = Products<F, NM, DEPTH>;
-  using T = FmtOf<F>;
+// Streams the products of jobs 0 to jobs - 1 through a wave: a step's loads are in flight during the MFMAs
+// of the step before, across the ends of jobs.  (With 16 waves on a CU two or three steps ahead are no
+// faster: bf16's first kernel 25.4 us for 24.9, mxfp4's second 27.1 for 25.4, e4m3's 93 for 91.)
+//
+// share(job, first, stride): the job's share of K, at least one step; start(job, products) sets its streams;
+// finish(job, sums) takes its sums.
+//
+// Every step loads, past the last one zeros that cost no memory access, so that the compiler's count of loads in
+// flight holds on every path.
+template <int F, int NM, int NX, typename Share, typename Start, typename Finish>
+__device__ __forceinline__ void stream(uint8_t* lds, int jobs, int row_bytes, Share&& share, Start&& start,
+                                       Finish&& finish) {
+  using P = Products<F, NM, NX>;
   if (jobs <= 0) return;
+  struct Cursor {   // a step of a job
+    int job, step, n, first, stride;
+    __device__ __forceinline__ int at() const { return (first + step * stride) * kStep; }
+  };
+  auto begin = [&](Cursor& c, int job) {
+    c.job = job;
+    c.step = 0;
+    share(job, c.first, c.stride);
+    c.n = P::steps(row_bytes, c.first, c.stride);
+  };
   P p;
-  int first = 0, stride = 1, load_job = 0, load_step = 0;
-  start(0, p, first, stride);
-  int load_steps = steps_of(0);
-  int use_job = 0, left = load_steps;   // of the job in use
-  auto get = [&](Step<F, NM>& b) {
-    if (load_job >= jobs) return;
-    const int at = T::kPieces == 2 ? (first + load_step * stride) * 128
-                                   : (first + (load_step >> 1) * stride) * 128 + (load_step & 1) * 64;
-    if (at + T::kStep <= p.row_bytes)
-      p.template load<true>(b, at);
-    else
-      p.template load<false>(b, at);
-    if (++load_step == load_steps) {
-      load_step = 0;
-      if (++load_job < jobs) {
-        start(load_job, p, first, stride);
-        load_steps = steps_of(load_job);
-      }
+  p.row_bytes = row_bytes;
+  Cursor get, now;
+  begin(get, 0);
+  begin(now, 0);
+  start(0, p);
+  uint32_t past = 0;
+  auto load = [&](Step<F, NM, NX>& b) {
+    p.load(b, get.at(), past);
+    if (get.step + 1 < get.n) {
+      ++get.step;
+    } else if (get.job + 1 < jobs) {
+      begin(get, get.job + 1);
+      start(get.job, p);
+    } else {
+      past = kPast;
     }
   };
-  Step<F, NM> b[DEPTH];
+  Step<F, NM, NX> b;
+  load(b);
   f32x4 acc[NM];
 #pragma unroll
   for (int m = 0; m < NM; ++m) acc[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < DEPTH; ++j) get(b[j]);
   while (true) {
+    if (b.left < kStep) P::end_row(b);
+    P::use(lds, b, acc);
+    // the loads stay behind the products of the step whose registers they take: hoisted, they need others
+    __builtin_amdgcn_sched_barrier(0);
+    load(b);
+    __builtin_amdgcn_sched_barrier(0);
+    if (++now.step < now.n) continue;
+    finish(now.job, acc);
+    if (now.job + 1 == jobs) return;
+    begin(now, now.job + 1);
 #pragma unroll
-    for (int j = 0; j < DEPTH; ++j) {
-      P::use(b[j], acc);
-      get(b[j]);
-      if (--left == 0) {
-        finish(use_job, acc);
-        if (++use_job == jobs) return;
-        left = steps_of(use_job);
-#pragma unroll
-        for (int m = 0; m < NM; ++m) acc[m] = f32x4{0, 0, 0, 0};
-      }
-    }
+    for (int m = 0; m < NM; ++m) acc[m] = f32x4{0, 0, 0, 0};
   }
 }
 
+// Calls f with the loads of activations that hold the tokens of the largest listed expert.
+template <int F, typename Fn>
+__device__ __forceinline__ void with_x_loads(int most, Fn&& f) {
+  constexpr int kBits = FmtOf<F>::kBits;
+  const int n = (most + FmtOf<F>::kXTokens - 1) / FmtOf<F>::kXTokens;
+  if (n <= 1) return f(std::integral_constant<int, 1>{});
+  if constexpr (kBits == 16) {
+    f(std::integral_constant<int, 2>{});
+  } else {
+    if (n <= 2) return f(std::integral_constant<int, 2>{});
+    if constexpr (kBits == 8) {
+      f(std::integral_constant<int, 4>{});
+    } else {
+      if (n <= 4) return f(std::integral_constant<int, 4>{});
+      f(std::integral_constant<int, 8>{});
+    }
+  }
+}
 template <int F>
-constexpr int kDepthUp = FmtOf<F>::kInt4 || F == kE4m3 ? 2 : 3;
-template <int F>
-constexpr int kDepthDown = FmtOf<F>::kInt4 || F == kE4m3 ? 3 : 4;
-// workgroups on a CU that the registers leave room for
-template <int F>
-constexpr int kUpGroups = F == kInt4x32 ? 3 : 4;
+constexpr int kMostXLds = FmtOf<F>::kBits == 16 ? 2 : 4;   // loads that go through LDS
+template <int F, int NM>
+constexpr int kWaveLds = Products<F, NM, kMostXLds<F>>::kLds;
 
-constexpr int kUpWaves = 4;
-constexpr int kDownWaves = 8;
-constexpr int kDownParts = 768;   // routed rows times shares of K that the second kernel's LDS holds
+constexpr int kWaves = 8;
+constexpr int kUpGroups = 512;     // workgroups of the first kernel: two on each of 256 CUs
+constexpr int kDownParts = 512;    // routed rows times shares of K that the second kernel's LDS holds
 
 struct UpArgs {
   const uint8_t* x;       // [T, H] bf16
@@ -289,7 +430,7 @@ struct UpArgs {
   const uint8_t* w;       // [E, 2I, H]
   const uint8_t* s;
   int T, H, I, E, k, valid, renorm;
-  int blocks;             // ceil(I / 16)
+  int blocks;             // ceil(I / 8)
   DecodePlan* plan;
   uint16_t* h;            // [T k, I] bf16
 };
@@ -303,31 +444,116 @@ __device__ __forceinline__ int scale_bytes(int K) {
   return 0;
 }
 
-// the streams of a wave whose lanes' weight rows are base + n, n below 2^32 bytes of weights on
-template <int F, int NM, int DEPTH>
-__device__ __forceinline__ void set_rows(Products<F, NM, DEPTH>& p, const uint8_t* w, const uint8_t* s,
-                                         const long long (&base)[NM], int n0, int n, int K) {
-  const int g = lane_id() >> 4, sb = scale_bytes<F>(K);
-  p.g = g;
-  p.row_bytes = K / FmtOf<F>::kVal * 16;
-  p.w_off = (uint32_t)n * (uint32_t)p.row_bytes + 16 * g;
-  p.s_off = (uint32_t)n * (uint32_t)sb + (F == kMxfp4 ? g : 0);
+// The streams of a wave on columns n0 to n0 + 7 of the listed experts `at` and `at` + 1 (past the list's end: of the
+// last one again).  Expert e's NM blocks of N weight rows of K channels begin at row e * NM * N; columns past N repeat
+// the last one.  N rows are below 2 GiB, and so are the activations, x_rows rows of K at x, of which `rows` has the tokens'.
+template <int F, int NM, int NX>
+__device__ __forceinline__ void set_rows(Products<F, NM, NX>& p, const DecodePlan& plan, int at, int n0, const uint8_t* w,
+                                         const uint8_t* s, int N, int K, const void* x, int x_rows,
+                                         const uint8_t (&rows)[kDecodeRows][8]) {
+  using P = Products<F, NM, NX>;
+  const int sb = scale_bytes<F>(K);
+  const int e[2] = {__builtin_amdgcn_readfirstlane(plan.expert[at]),
+                    __builtin_amdgcn_readfirstlane(plan.expert[min(at + 1, plan.entries - 1)])};
+  p.w_bytes = (uint32_t)N * (uint32_t)p.row_bytes;
+  p.w_off = (uint32_t)min(n0 + (lane_id() >> 3), N - 1) * (uint32_t)p.row_bytes + P::w_lane();
 #pragma unroll
-  for (int m = 0; m < NM; ++m) {
-    p.w[m] = w + base[m] * p.row_bytes;
-    // e4m3: the block row of columns n0 to n0 + 15
-    p.s[m] = F == kE4m3 ? s + ((base[m] + n0) >> 7) * sb : s + base[m] * sb;
+  for (int m = 0; m < NM; ++m)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p.w[m][i] = w + ((long long)e[i] * NM + m) * N * p.row_bytes;
+  const int c = lane_id() & 15;
+  const long long row = ((long long)(c < 8 ? e[0] : e[1]) * NM + P::s_matrix()) * N + min(n0 + (c & 7), N - 1);
+  p.s = s + (F == kE4m3 ? row >> 7 : row) * sb;
+  p.x = static_cast<const uint8_t*>(x);
+  p.x_bytes = (uint32_t)(x_rows * K) * 2;
+  auto row_of = [&](int half, int token, int byte) {
+    const int entry = at + half;
+    return entry < plan.entries && token < plan.count[entry] ? (uint32_t)rows[entry][token] * (uint32_t)K * 2 + byte : kPast;
+  };
+  if constexpr (P::kDirect) {
+    p.x_off[0] = row_of(c >> 3, c & 7, P::x_lane());
+  } else {
+#pragma unroll
+    for (int i = 0; i < NX; ++i) p.x_off[i] = row_of(P::x_row(i) & 1, P::x_row(i) >> 1, P::x_load());
   }
 }
 
-// Routes the tokens and lists the experts that have rows, in the order of their first row, with their
-// rows in ascending order.  `words`: E, of LDS, twice.
+// Top-k routing of one token by a wave, with the ids and weights of route_device.h's route_token: k rounds of a
+// maximum over the lanes.  Logits are compared as integers that order as they do, so that a step of
+// the maximum is one instruction; the lowest id of equal ones is the first lane that has the maximum, of the first
+// 64 experts that have it.  (Every workgroup routes every token: 16 of 128 experts, 8 each, were half of the first kernel's
+// instructions with route_token.)
 template <int EPL>
-__device__ __forceinline__ void make_plan(const UpArgs& a, DecodePlan& plan, uint32_t* tokens, uint32_t* index, int* ids) {
+__device__ __forceinline__ void route(const UpArgs& a, int t, int* ids, float* weights) {
+  const int lane = lane_id();
+  const float* row = a.logits + (size_t)t * a.E;
+  uint32_t key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + kWave * i;
+    const uint32_t b = __float_as_uint((e < a.E ? row[e] : 0.0f) + 0.0f);   // -0 becomes 0
+    key[i] = e < a.E ? max(b ^ ((uint32_t)((int)b >> 31) | 0x80000000u), 1u) : 0u;   // 0: not there, or taken
+  }
+  auto value = [](uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); };
+  uint32_t all[EPL];   // the softmax over all logits needs them again
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) all[i] = key[i];
+  uint32_t my_key = 0, top = 0;
+  int my_id = 0;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, m, 0x128, 0xf, 0xf, false));   // row_ror by 8, 4, 2, 1
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, m, 0x124, 0xf, 0xf, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, m, 0x122, 0xf, 0xf, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, m, 0x121, 0xf, 0xf, false));
+    const uint32_t best = max(max((uint32_t)__builtin_amdgcn_readlane(m, 0), (uint32_t)__builtin_amdgcn_readlane(m, 16)),
+                              max((uint32_t)__builtin_amdgcn_readlane(m, 32), (uint32_t)__builtin_amdgcn_readlane(m, 48)));
+    bool found = false;
+    int id = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint64_t who = __ballot(key[i] == best);
+      const bool here = !found && who != 0;
+      const int l = __builtin_ctzll(who | (1ull << 63));
+      id = here ? kWave * i + l : id;
+      key[i] = here && lane == l ? 0u : key[i];
+      found |= here;
+    }
+    if (j == 0) top = best;
+    if (lane == j) {
+      my_key = best;
+      my_id = id;
+    }
+  }
+  const float ex = lane < a.k ? expf(value(my_key) - value(top)) : 0.0f;
+  float denom;
+  if (a.renorm) {
+    denom = wave_sum(ex);
+  } else {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (lane + kWave * i < a.E) s += expf(value(all[i]) - value(top));
+    denom = wave_sum(s);
+  }
+  if (lane < a.k) {
+    const int r = t * a.k + lane;
+    ids[r] = r < a.valid ? my_id : a.E;
+    weights[r] = r < a.valid ? ex / denom : 0.0f;
+  }
+}
+
+// Routes the tokens and lists the experts that have rows, in the order of their first (and their ninth) row, with their
+// rows in ascending order.
+template <int EPL>
+__device__ __forceinline__ void make_plan(const UpArgs& a, DecodePlan& plan, uint32_t* tokens, uint16_t (*index)[2],
+                                          int* ids) {
   const int wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < a.E; e += kUpWaves * kWave) tokens[e] = 0;
-  for (int t = wave; t < a.T; t += kUpWaves)
-    route_token<EPL>(a.logits, t, a.E, a.k, a.valid, a.renorm, ids, plan.weight);
+  for (int e = threadIdx.x; e < a.E; e += kWaves * kWave) tokens[e] = 0;
+  if (threadIdx.x == 0) plan.most = 1;
+  for (int t = wave; t < a.T; t += kWaves) route<EPL>(a, t, ids, plan.weight);
   __syncthreads();
   const int r = threadIdx.x;   // T k <= 256
   const int e = r < a.T * a.k ? ids[r] : a.E;
@@ -337,98 +563,133 @@ __device__ __forceinline__ void make_plan(const UpArgs& a, DecodePlan& plan, uin
   __syncthreads();
   const uint32_t mine = live ? tokens[e] : 0;
   const int rank = __popc(mine & ((1u << t) - 1));
-  const bool first = live && rank == 0;
-  // position among the first rows of experts: this wave's by ballot, the waves' by LDS
+  const bool first = live && (rank & 7) == 0;
+  // position among the first rows of entries: this wave's by ballot, the waves' by LDS
   const uint64_t firsts = __ballot(first);
   if (lane_id() == 0) ids[kDecodeRows + wave] = __popcll(firsts);
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < kUpWaves; ++i) {
+  for (int i = 0; i < kWaves; ++i) {
     const int n = ids[kDecodeRows + i];
     before += i < wave ? n : 0;
     all += n;
   }
   if (first) {
     const int at = before + __popcll(firsts & ((1ull << lane_id()) - 1));
-    index[e] = at;
+    index[e][rank >> 3] = (uint16_t)at;
     plan.expert[at] = (uint16_t)e;
-    plan.count[at] = (uint8_t)__popc(mine);
+    plan.count[at] = (uint8_t)min(__popc(mine) - rank, 8);
+    atomicMax(&plan.most, min(__popc(mine), 8));
   }
-  if (threadIdx.x == 0) plan.active = all;
+  if (threadIdx.x == 0) plan.entries = all;
   __syncthreads();
-  if (live) plan.rows[index[e]][rank] = (uint8_t)r;
+  if (live) {
+    const int at = index[e][rank >> 3];
+    plan.id[r] = (uint16_t)e;
+    plan.rows[at][rank & 7] = (uint8_t)r;
+    plan.tokens[at][rank & 7] = (uint8_t)t;
+  }
   __syncthreads();
 }
 
 template <int F, int EPL>
-__global__ __launch_bounds__(kUpWaves * kWave, kUpGroups<F>) void decode_up_kernel(UpArgs a) {
+__global__ __launch_bounds__(kWaves * kWave, 4) void decode_up_kernel(UpArgs a) {
   using T = FmtOf<F>;
   __shared__ DecodePlan plan;
-  __shared__ uint32_t tokens[EPL * kWave], index[EPL * kWave];
-  __shared__ int ids[kDecodeRows + kUpWaves];
-  __shared__ float part[kUpWaves][2][16][17];
-  make_plan<EPL>(a, plan, tokens, index, ids);
+  // The waves' LDS.  Before the streams the lists of make_plan(), at an item's end its sums.
+  struct Lists {
+    uint32_t tokens[EPL * kWave];
+    uint16_t index[EPL * kWave][2];
+    int ids[kDecodeRows + kWaves];
+  };
+  __shared__ union {
+    Lists lists;
+    __attribute__((aligned(16))) uint8_t lines[kWaves][kWaveLds<F, 2>];
+  } lds;
+  static_assert(sizeof(lds) + sizeof(DecodePlan) <= 80 << 10, "two workgroups on a CU");
+  make_plan<EPL>(a, plan, lds.lists.tokens, lds.lists.index, lds.lists.ids);
   if (blockIdx.x == 0) {   // for the second kernel
     const uint4* from = reinterpret_cast<const uint4*>(&plan);
-    for (int i = threadIdx.x; i < (int)(sizeof(DecodePlan) / 16); i += kUpWaves * kWave)
+    for (int i = threadIdx.x; i < (int)(sizeof(DecodePlan) / 16); i += kWaves * kWave)
       reinterpret_cast<uint4*>(a.plan)[i] = from[i];
   }
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int active = __builtin_amdgcn_readfirstlane(plan.active);
-  const int items = active * a.blocks;   // (expert, 16 columns): blockIdx.x, + gridDim.x, ...
-  const int jobs = items > (int)blockIdx.x ? (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  const int entries = __builtin_amdgcn_readfirstlane(plan.entries);
+  const int items = (entries + 1) / 2 * a.blocks;   // (two experts, 8 columns)
+  const int units = (a.H / T::kVal * 16 + kStep - 1) / kStep;
+  // Waves that share an item's K: more while each has three steps or where waves are left over
+  int split = 1;
+  while (split < kWaves && 2 * split <= units &&
+         (units >= 6 * split || 2 * split * items <= (int)gridDim.x * kWaves))
+    split *= 2;
+  const int share = wave % split, group = wave / split;
+  const int groups = (int)gridDim.x * (kWaves / split);
+  const int rounds = (items + groups - 1) / groups;
+  const int my_first = (int)blockIdx.x * (kWaves / split) + group;
+  const int jobs = items > my_first ? (items - my_first + groups - 1) / groups : 0;   // rounds or one less
   auto item_of = [&](int job, int& at, int& n0) {
-    const int item = (int)blockIdx.x + job * (int)gridDim.x;
-    at = item / a.blocks;
-    n0 = (item - at * a.blocks) * 16;
+    const int item = my_first + job * groups, pair = item / a.blocks;
+    at = 2 * pair;
+    n0 = (item - pair * a.blocks) * 8;
   };
-  const int steps = Products<F, 2, 1>::steps(a.H / T::kVal * 16, wave, kUpWaves);
-  // the waves' sums of an item: joined by every thread for one token and column
-  auto finish = [&](int job, const f32x4 (&acc)[2]) {
+  auto store = [&](int at, int half, int token, int col, float gate, float up) {
+    if (at + half < entries && token < plan.count[at + half] && col < a.I) {
+      if (F == kInt8) {
+        const float* s = reinterpret_cast<const float*>(a.s) + (long long)plan.expert[at + half] * 2 * a.I + col;
+        gate *= s[0];
+        up *= s[a.I];
+      }
+      a.h[(long long)plan.rows[at + half][token] * a.I + col] = f32_to_bf16_bits(silu_mul(gate, up));
+    }
+  };
+  const int half = (lane >> 3) & 1, token0 = 4 * ((lane >> 4) & 1);
+  const bool mine = lane >> 5 == half;   // the lane's sums are of a token and its own expert
+  auto finish = [&](int job, const f32x4 (&v)[2]) {
     int at, n0;
     item_of(job, at, n0);
-    const int count = plan.count[at];
+    if (split == 1) {
+      if (mine)
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+        for (int r = 0; r < 4; ++r) store(at, half, token0 + r, n0 + (lane & 7), v[0][r], v[1][r]);
+      return;
+    }
+    auto part = [&](int w) { return reinterpret_cast<float(*)[2][8][8]>(lds.lines[w]); };   // [gate or up]
+    if (mine)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][m][4 * (lane >> 4) + r][lane & 15] = acc[m][r];
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part(wave)[m][half][token0 + r][lane & 7] = v[m][r];
     __syncthreads();
-    const int j = threadIdx.x >> 4, c = n0 + (threadIdx.x & 15);
-    if (j < count && c < a.I) {
-      float v[2];
+    const int u = share * kWave + lane;   // expert, token and column
+    if (u < 128) {
+      float sum[2] = {0.0f, 0.0f};
+      for (int i = 0; i < split; ++i)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        v[m] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kUpWaves; ++i) v[m] += part[i][m][j][threadIdx.x & 15];
-        if (F == kInt8)
-          v[m] *= reinterpret_cast<const float*>(a.s)[(long long)plan.expert[at] * 2 * a.I + m * a.I + c];
-      }
-      a.h[(long long)plan.rows[at][j] * a.I + c] = f32_to_bf16_bits(silu_mul(v[0], v[1]));
+        for (int m = 0; m < 2; ++m) sum[m] += part(wave - share + i)[m][u >> 6][(u >> 3) & 7][u & 7];
+      store(at, u >> 6, (u >> 3) & 7, n0 + (u & 7), sum[0], sum[1]);
     }
     __syncthreads();
   };
-  if (steps == 0) {   // a row of fewer units than waves: nothing to add
-    const f32x4 none[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-    for (int job = 0; job < jobs; ++job) finish(job, none);
-    return;
+  with_x_loads<F>(__builtin_amdgcn_readfirstlane(plan.most), [&](auto nx) {
+    constexpr int NX = decltype(nx)::value;
+    stream<F, 2, NX>(
+        lds.lines[wave], jobs, a.H / T::kVal * 16,
+        [&](int, int& first, int& stride) {
+          first = share;
+          stride = split;
+        },
+        [&](int job, auto& p) {
+          int at, n0;
+          item_of(job, at, n0);
+          set_rows(p, plan, at, n0, a.w, a.s, a.I, a.H, a.x, a.T, plan.tokens);
+        },
+        finish);
+  });
+  if (split > 1 && jobs < rounds) {   // the other groups' last item
+    __syncthreads();
+    __syncthreads();
   }
-  stream<F, 2, kDepthUp<F>>(
-      jobs,
-      [&](int job, auto& p, int& first, int& stride) {
-        int at, n0;
-        item_of(job, at, n0);
-        const int e = __builtin_amdgcn_readfirstlane(plan.expert[at]), count = plan.count[at];
-        const long long row = (long long)e * 2 * a.I;
-        // columns past I repeat the last one, tokens past the expert's its last
-        set_rows(p, a.w, a.s, {row, row + a.I}, n0, min(n0 + (lane & 15), a.I - 1), a.H);
-        p.x = a.x;
-        p.x_off = (uint32_t)(plan.rows[at][min(lane & 15, count - 1)] / a.k) * (uint32_t)a.H * 2 + p.x_lane(p.g);
-        first = wave;
-        stride = kUpWaves;
-      },
-      [&](int) { return steps; }, finish);
 }
 
 struct DownArgs {
@@ -442,57 +703,56 @@ struct DownArgs {
 };
 
 template <int F>
-__global__ __launch_bounds__(kDownWaves * kWave, 4) void decode_down_kernel(DownArgs a) {
+__global__ __launch_bounds__(kWaves * kWave, 4) void decode_down_kernel(DownArgs a) {
   using T = FmtOf<F>;
   __shared__ DecodePlan plan;
-  __shared__ float part[kDownParts][16];
-  for (int i = threadIdx.x; i < (int)(sizeof(DecodePlan) / 16); i += kDownWaves * kWave)
+  __shared__ float part[kDownParts][8];
+  __shared__ __attribute__((aligned(16))) uint8_t lines[kWaves][kWaveLds<F, 1>];
+  static_assert(sizeof(plan) + sizeof(part) + sizeof(lines) <= 80 << 10, "two workgroups on a CU");
+  for (int i = threadIdx.x; i < (int)(sizeof(DecodePlan) / 16); i += kWaves * kWave)
     reinterpret_cast<uint4*>(&plan)[i] = reinterpret_cast<const uint4*>(a.plan)[i];
   __syncthreads();
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16, n = min(n0 + (lane & 15), a.H - 1);
-  const int active = __builtin_amdgcn_readfirstlane(plan.active);
-  // Shares of K: about four jobs a wave, at least one unit each.  shares * valid <= kDownParts: an active
-  // expert has up to 16 of the valid rows, so while active < 16 it is at most 16 * (32 + active - 1), up to
-  // 31 two shares of 256 rows, then one.
-  const int row_bytes = a.I / T::kVal * 16;
-  const int shares = active ? min((4 * kDownWaves + active - 1) / active, (row_bytes + 127) >> 7) : 1;
-  const int units = active * shares;
-  stream<F, 1, kDepthDown<F>>(
-      units > wave ? (units - wave + kDownWaves - 1) / kDownWaves : 0,
-      [&](int job, auto& p, int& first, int& stride) {
-        const int unit = wave + job * kDownWaves, at = unit / shares;
-        const int e = __builtin_amdgcn_readfirstlane(plan.expert[at]), count = plan.count[at];
-        set_rows(p, a.w, a.s, {(long long)e * a.H}, n0, n, a.I);
-        p.x = reinterpret_cast<const uint8_t*>(a.h);
-        p.x_off = (uint32_t)plan.rows[at][min(lane & 15, count - 1)] * (uint32_t)a.I * 2 + p.x_lane(p.g);
-        first = unit - at * shares;
-        stride = shares;
-      },
-      [&](int job) {
-        const int unit = wave + job * kDownWaves;
-        return Products<F, 1, 1>::steps(row_bytes, unit - unit / shares * shares, shares);
-      },
-      [&](int job, const f32x4 (&acc)[1]) {
-        const int unit = wave + job * kDownWaves, at = unit / shares, share = unit - at * shares;
-        const int count = plan.count[at];
-        float scale = 1.0f;
-        if (F == kInt8) scale = reinterpret_cast<const float*>(a.s)[(long long)plan.expert[at] * a.H + n];
+  const int n0 = blockIdx.x * 8;
+  const int entries = __builtin_amdgcn_readfirstlane(plan.entries), pairs = (entries + 1) / 2;
+  // Shares of K: about four jobs a wave, at least one unit each.  shares * valid <= kDownParts: a pair
+  // has up to 16 of the valid rows, all of them at most 256.
+  const int units = (a.I / T::kVal * 16 + kStep - 1) / kStep;
+  const int shares = pairs ? max(min(4 * kWaves / pairs, units), 1) : 1;
+  const int all = pairs * shares;
+  with_x_loads<F>(__builtin_amdgcn_readfirstlane(plan.most), [&](auto nx) {
+    constexpr int NX = decltype(nx)::value;
+    stream<F, 1, NX>(
+        lines[wave], all > wave ? (all - wave + kWaves - 1) / kWaves : 0, a.I / T::kVal * 16,
+        [&](int job, int& first, int& stride) {
+          const int unit = wave + job * kWaves;
+          first = unit - unit / shares * shares;
+          stride = shares;
+        },
+        [&](int job, auto& p) {
+          const int at = 2 * ((wave + job * kWaves) / shares);
+          set_rows(p, plan, at, n0, a.w, a.s, a.H, a.I, a.h, a.T * a.k, plan.rows);
+        },
+        [&](int job, const f32x4 (&acc)[1]) {
+          const int unit = wave + job * kWaves, pair = unit / shares, share = unit - pair * shares;
+          const int half = (lane >> 3) & 1, token0 = 4 * ((lane >> 4) & 1), at = 2 * pair + half;
+          if (lane >> 5 != half || at >= entries) return;
+          const int count = plan.count[at];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 4 * (lane >> 4) + r;
-          if (j < count) part[share * a.valid + plan.rows[at][j]][lane & 15] = F == kInt8 ? acc[0][r] * scale : acc[0][r];
-        }
-      });
+          for (int r = 0; r < 4; ++r)
+            if (token0 + r < count) part[share * a.valid + plan.rows[at][token0 + r]][lane & 7] = acc[0][r];
+        });
+  });
   __syncthreads();
-  const int t = threadIdx.x >> 4, c = n0 + (threadIdx.x & 15);
+  const int t = threadIdx.x >> 3, c = n0 + (threadIdx.x & 7);
   if (t >= a.T || c >= a.H) return;
   float v = 0.0f;
   for (int j = 0; j < a.k; ++j) {
     const int r = t * a.k + j;
     if (r >= a.valid) break;   // rows from `valid` on are not routed
     float y = 0.0f;
-    for (int i = 0; i < shares; ++i) y += part[i * a.valid + r][threadIdx.x & 15];
+    for (int i = 0; i < shares; ++i) y += part[i * a.valid + r][threadIdx.x & 7];
+    if (F == kInt8) y *= reinterpret_cast<const float*>(a.s)[(long long)plan.id[r] * a.H + c];
     v = fmaf(plan.weight[r], y, v);
   }
   const long long o = (long long)t * a.H + c;
@@ -504,10 +764,10 @@ __global__ __launch_bounds__(kDownWaves * kWave, 4) void decode_down_kernel(Down
 
 template <int F, int EPL>
 hipError_t launch_up(const UpArgs& a, hipStream_t stream) {
-  // what fits on 256 CUs at once
-  const long long items = (long long)std::min(a.valid, a.E) * a.blocks;
-  const int grid = (int)std::max(1ll, std::min<long long>(items, 256 * kUpGroups<F>));
-  hipLaunchKernelGGL((decode_up_kernel<F, EPL>), dim3(grid), dim3(kUpWaves * kWave), 0, stream, a);
+  // an expert is listed once for eight of its rows
+  const long long items = ((long long)std::min(a.valid, a.E + a.valid / 8) + 1) / 2 * a.blocks;
+  const int grid = (int)std::max(1ll, std::min<long long>(items, kUpGroups));
+  hipLaunchKernelGGL((decode_up_kernel<F, EPL>), dim3(grid), dim3(kWaves * kWave), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -515,13 +775,11 @@ template <int F>
 hipError_t launch_both(const UpArgs& u, const DownArgs& d, hipStream_t stream) {
   hipError_t e;
   switch ((u.E + kWave - 1) / kWave) {
-    case 1: e = launch_up<F, 1>(u, stream); break;
-    case 2: e = launch_up<F, 2>(u, stream); break;
-    case 3: case 4: e = launch_up<F, 4>(u, stream); break;
+    case 1: case 2: case 3: case 4: e = launch_up<F, 4>(u, stream); break;
     default: e = launch_up<F, 16>(u, stream); break;
   }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(decode_down_kernel<F>, dim3((d.H + 15) / 16), dim3(kDownWaves * kWave), 0, stream, d);
+  hipLaunchKernelGGL(decode_down_kernel<F>, dim3((d.H + 7) / 8), dim3(kWaves * kWave), 0, stream, d);
   return hipGetLastError();
 }
 
@@ -542,7 +800,7 @@ hipError_t launch_decode(const DecodeLaunch& q, hipStream_t stream) {
   u.k = q.k;
   u.valid = q.valid;
   u.renorm = q.renorm;
-  u.blocks = (q.I + 15) / 16;
+  u.blocks = (q.I + 7) / 8;
   u.plan = static_cast<DecodePlan*>(q.plan);
   u.h = static_cast<uint16_t*>(q.h);
   DownArgs d{};

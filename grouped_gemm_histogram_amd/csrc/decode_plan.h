@@ -8,13 +8,17 @@ namespace moe {
 constexpr int kDecodeTokens = 16;               // tokens of a call
 constexpr int kDecodeRows = kDecodeTokens * 16; // routed rows
 
+// The list of experts that have rows, an expert once for each eight of them.
 struct alignas(16) DecodePlan {
-  int active;                           // experts that have rows
-  int unused[3];
-  float weight[kDecodeRows];            // of each routed row
-  uint16_t expert[kDecodeRows];         // the active experts
-  uint8_t count[kDecodeRows];           // rows of each
-  uint8_t rows[kDecodeRows][kDecodeTokens];   // their routed rows, ascending
+  int entries;
+  int most;                         // rows of the largest of them
+  int unused[2];
+  float weight[kDecodeRows];        // of each routed row
+  uint16_t id[kDecodeRows];         // its expert
+  uint16_t expert[kDecodeRows];     // of each entry
+  uint8_t count[kDecodeRows];       // its rows, 1 to 8
+  uint8_t rows[kDecodeRows][8];     // the routed rows, ascending
+  uint8_t tokens[kDecodeRows][8];   // and their tokens
 };
 
 }  // namespace moe

@@ -560,7 +560,9 @@ size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, 
  *                                      multiples of 16
  *                MOE_WEIGHTS_INT4, MOE_WEIGHTS_MXFP4
  *                                      codes and scales of moe_quantize_fourbit with
- *                                      `group`; multiples of 32 and of group
+ *                                      `group`; multiples of 32 and of group, at
+ *                                      least 128 (less is MOE_ERR_UNSUPPORTED)
+ *                One expert's W13 spans under 4 GiB.
  *   router_logits, num_valid_rows, renormalize: as for moe_route_topk.
  *   out          [T, H] of out_dtype (MOE_F32 or MOE_BF16); tokens without a valid row
  *                get exact zeros.

@@ -130,9 +130,12 @@ def test_sizes(fmt, T, H, I, E, k, valid):
     if u == 128 and E > 40:
         E = 20                                     # the host's products
         k = min(k, E)
-    say("decode", fmt, T, H * u, I * u, E, k, valid)
-    c = Case(fmt, T, H * u, I * u, E, k, seed=T * 31 + E)
-    got, ref = c.check(valid, renormalize=T != 5, out=torch.float32 if H % 2 else torch.bfloat16)
+    H, I = H * u, I * u
+    if "4" in fmt:                                 # 4-bit rows have at least 128 channels
+        H, I = max(H, 128), max(I, 128)
+    say("decode", fmt, T, H, I, E, k, valid)
+    c = Case(fmt, T, H, I, E, k, seed=T * 31 + E)
+    got, ref = c.check(valid, renormalize=T != 5, out=torch.float32 if T % 2 else torch.bfloat16)
     assert (np32(got)[np.abs(ref).sum(axis=1) == 0] == 0).all()
 
 
@@ -260,6 +263,9 @@ def test_empty_and_refused():
         g.forward_decode(f(1, 16), lg(1, 4), f(4, 32, 16), f(4, 16, 24), 2)
     with pytest.raises(ValueError):
         g.forward_decode(f(1, 16), lg(1, 4), f(4, 32, 16), f(4, 16, 16), 2, w13_scale=lg(4, 32), w2_scale=lg(4, 16))
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=DEV)
+    with pytest.raises(RuntimeError, match="128 channels"):
+        g.forward_decode(f(1, 96), lg(1, 4), u8(4, 256, 48), u8(4, 96, 64), 2, w13_scale=u8(4, 256, 3), w2_scale=u8(4, 96, 4))
     i8 = lambda *s: torch.zeros(*s, dtype=torch.int8, device=DEV)
     with pytest.raises(ValueError):
         g.forward_decode(f(1, 16), lg(1, 4), i8(4, 32, 16), i8(4, 16, 16), 2)
