@@ -7,7 +7,9 @@
 //     p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 //
 // The step is bound by HBM: an element of bf16 parameters with bf16 gradients moves 22 bytes with
-// f32 states and 10 with 8-bit ones.  A lane therefore takes 8 consecutive elements, so that
+// f32 states and 10 with 8-bit ones.  With f32 states, an f32 copy and f32 gradients 80 million elements take 498 us, 4.5
+// TB/s (a copy of as many bytes runs at 4.8 to 5.1); with 8-bit states and rounding by chance 100 million
+// elements take 229 us, 4.4 TB/s, with the VALU busy for most of it (94 instructions an element).  A lane therefore takes 8 consecutive elements, so that
 // every access is 8 or 16 bytes a lane and 16 lanes hold a block of 128 elements: the block's largest
 // value is a reduction over 16 lanes by rotations, without LDS.  A workgroup takes 2048 elements of one
 // tensor, found by a binary search over the first workgroups of up to 64 tensors that travel in the
@@ -72,26 +74,26 @@ __device__ __forceinline__ uint32_t piece16(const uint4& r, int j) {
 // mantissa bits below e4m3's three are a 20-bit fraction of a step, and the piece, centred in its
 // share of 16, is added to them.  Codes below the smallest normal (2^-6) have its step, so 2^-6 is added to
 // round there and taken off the code.
+//
+// No branches here: a lane's early return for each of 16 values took as many instructions as the rounding.
+template <bool kSigned, bool kFinite>
 __device__ __forceinline__ uint32_t e4m3_by_chance(float x, uint32_t piece) {
   const float a = fabsf(x);
-  if (!(a < INFINITY)) return 0x7fu;
   const bool small = a < 0.015625f;
-  const uint32_t b = __float_as_uint(small ? a + 0.015625f : a) + (piece << 4) + 8u;
-  const uint32_t code = (b >> 20) - (small ? 968u : 960u);
-  return min(code, 126u) | ((__float_as_uint(x) >> 24) & 0x80u);
+  const uint32_t b = __float_as_uint(small ? a + 0.015625f : a) + (piece << 4) + (small ? 8u - (968u << 20) : 8u - (960u << 20));
+  uint32_t code = min(b >> 20, 126u);
+  if (kSigned) code |= (__float_as_uint(x) >> 24) & 0x80u;
+  return kFinite || a < INFINITY ? code : 0x7fu;
 }
 
-// 8 codes of a block of 128 elements (16 lanes): scale = amax * (1 / 448).  kLeast: values above zero keep code 1.
-template <bool kLeast>
+// 8 codes of a block of 128 elements (16 lanes): scale = amax * (1 / 448).  kLeast: no value is negative, and those
+// above zero keep code 1.  kFinite: there are no infinities or NaN.
+template <bool kLeast, bool kFinite>
 __device__ __forceinline__ uint2 pack_block(const float (&x)[kPer], const uint4& bits, bool chance, float& scale) {
 #pragma clang fp contract(off)
   float amax = 0.0f;
-  bool bad = false;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    amax = fmaxf(amax, fabsf(x[j]));
-    bad |= x[j] != x[j];
-  }
+  for (int j = 0; j < kPer; ++j) amax = fmaxf(amax, fabsf(x[j]));   // without NaN: the codes keep those
   auto rotated = [](float f, auto by) {   // row_ror:by
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(f), 0x120 + decltype(by)::value, 0xf, 0xf, false));
   };
@@ -106,22 +108,16 @@ __device__ __forceinline__ uint2 pack_block(const float (&x)[kPer], const uint4&
 #pragma unroll
   for (int j = 0; j < kPer; j += 2) {
     const float a = x[j] * inv, b = x[j + 1] * inv;
+    const uint32_t la = kLeast && x[j] > 0.0f && some ? 1u : 0u, lb = kLeast && x[j + 1] > 0.0f && some ? 1u : 0u;
     uint32_t c;
     if (chance) {
-      c = e4m3_by_chance(a, piece16(bits, j)) | e4m3_by_chance(b, piece16(bits, j + 1)) << 8;
+      c = max(e4m3_by_chance<!kLeast, kFinite>(a, piece16(bits, j)), la) |
+          max(e4m3_by_chance<!kLeast, kFinite>(b, piece16(bits, j + 1)), lb) << 8;
     } else {
       c = cvt_e4m3x2(a, b);
-    }
-    if (kLeast) {   // x >= 0: no sign bits
-      if (x[j] > 0.0f && some && !(c & 0xffu)) c |= 1u;
-      if (x[j + 1] > 0.0f && some && !(c & 0xff00u)) c |= 0x100u;
+      if (kLeast) c = max(c & 0xffu, la) | max(c >> 8 & 0xffu, lb) << 8;
     }
     w[j >> 2] |= c << (8 * (j & 2));
-  }
-  if (bad) {   // NaN elements keep the code of NaN
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (x[j] != x[j]) w[j >> 2] |= 0x7fu << (8 * (j & 3));
   }
   return make_uint2(w[0], w[1]);
 }
@@ -164,6 +160,34 @@ __device__ __forceinline__ void store8(void* p, long long at, int n, const float
     const float lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
     store_chunk<T, false>(q, chunk_from_f32<T>(lo), n);
     store_chunk<T, false>(q + 4, chunk_from_f32<T>(hi), n - 4);
+  }
+}
+
+// u = sqrt(v), rounded to nearest.  Goldschmidt's iteration on a 1-ulp reciprocal root and Markstein's last
+// correction by the exact residual take 10 instructions for sqrtf's 16; they need v's residual, 2^-48 v, to be
+// a normal number, so a wave with a smaller v above zero (or an infinite one) takes sqrtf.
+__device__ __forceinline__ void roots(const float (&v)[kPer], float (&u)[kPer]) {
+#pragma clang fp contract(off)
+  uint32_t least = 0xffffffffu;
+  float most = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    least = min(least, __float_as_uint(v[j]) - 1u);   // zeros (and negative values, whose root is NaN) pass
+    most = fmaxf(most, v[j]);
+  }
+  if (__any(least < 0x0f800000u - 1u || !(most < INFINITY))) {   // 2^-96
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) u[j] = sqrtf(v[j]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const float y = fminf(__builtin_amdgcn_rsqf(v[j]), 0x1p60f);   // of zero: its products with zero are zeros
+    float s = v[j] * y, h = 0.5f * y;
+    const float e = fmaf(-s, h, 0.5f);
+    s = fmaf(s, e, s);
+    h = fmaf(h, e, h);
+    u[j] = fmaf(fmaf(-s, s, v[j]), h, s);
   }
 }
 
@@ -212,10 +236,20 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
     const float gj = g[j] * gs;
     m[j] = m[j] * a.beta1 + gj * a.rest1;
     v[j] = v[j] * a.beta2 + (gj * gj) * a.rest2;
-    u[j] = sqrtf(v[j]);
+  }
+  roots(v, u);
+  float all = 0.0f;   // finite only if every result is
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
     const float upd = m[j] / (u[j] * root + a.eps);
     p[j] = p[j] * decay - upd * step_size;
-    if (S8 && j >= n) m[j] = u[j] = 0.0f;   // the rest of a tensor's last block
+    all += fabsf(p[j]) + (S8 ? fabsf(m[j]) + u[j] : 0.0f);
+  }
+  const bool finite = !__any(!(all < INFINITY));   // uniform: the few cases of infinities and NaN apart
+  if (S8 && n < kPer) {   // the rest of a tensor's last block
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j >= n) m[j] = u[j] = 0.0f;
   }
   uint4 bits = make_uint4(0, 0, 0, 0);
   const bool chance = a.rng != nullptr;
@@ -226,9 +260,15 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const uint32_t b = __float_as_uint(p[j]);
-      // infinities and NaN keep their upper half (a NaN its quiet bit)
-      const uint32_t up = fabsf(p[j]) < INFINITY ? b + piece16(bits, j) : (p[j] == p[j] ? b : b | 0x400000u);
-      w[j >> 1] |= (up >> 16) << (16 * (j & 1));
+      w[j >> 1] |= (b + piece16(bits, j)) >> 16 << (16 * (j & 1));
+    }
+    if (!finite) {   // infinities and NaN keep their upper half (a NaN its quiet bit)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (fabsf(p[j]) < INFINITY) continue;
+        const uint32_t b = __float_as_uint(p[j]) | (p[j] == p[j] ? 0u : 0x400000u);
+        w[j >> 1] = (w[j >> 1] & 0xffffu << (16 - 16 * (j & 1))) | b >> 16 << (16 * (j & 1));
+      }
     }
     store_chunk<uint16_t, false>(static_cast<uint16_t*>(s.p) + at, make_uint4(w[0], w[1], w[2], w[3]), n);
   } else {
@@ -236,8 +276,14 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
   }
   if constexpr (S8) {
     float sm, sv;
-    const uint2 cm = pack_block<false>(m, bits, chance, sm);
-    const uint2 cv = pack_block<true>(u, bits, chance, sv);
+    uint2 cm, cv;
+    if (finite) {
+      cm = pack_block<false, true>(m, bits, chance, sm);
+      cv = pack_block<true, true>(u, bits, chance, sv);
+    } else {
+      cm = pack_block<false, false>(m, bits, chance, sm);
+      cv = pack_block<true, false>(u, bits, chance, sv);
+    }
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + sat) = cm;
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + sat) = cv;
     if ((threadIdx.x & 15) == 0) {
