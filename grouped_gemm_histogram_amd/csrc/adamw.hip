@@ -346,7 +346,7 @@ hipError_t launch_adamw(const AdamwLaunch& q, hipStream_t stream) {
     const long long n = q.n[i];
     if (n > 0) {
       const long long mine = (n + kChunk - 1) / kChunk;
-      if (a.count == kTensors || blocks + mine > 0x7fffffffll) flush();
+      if (a.count == kTensors || blocks + mine >= (1ll << 32) / kThreads) flush();   // n <= 2^34
       a.slot[a.count] = Slot{q.param[i], q.grad[i], n, start};
       a.first[a.count++] = (int)blocks;
       blocks += mine;

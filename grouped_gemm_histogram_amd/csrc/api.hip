@@ -1221,11 +1221,25 @@ moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, c
 
 namespace {
 
-moe_status_t check_decode(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, moe_weights_t format, int32_t group) {
+constexpr int64_t kDecodeMaxWidth = 1 << 24;   // H and I: a launch has H / 8 workgroups of 512 threads
+
+// sizes that some format takes
+moe_status_t check_decode_sizes(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
   if (moe_status_t s = check_experts(E, k)) return s;
-  MOE_REQUIRE(T >= 0 && H > 0 && I > 0 && H <= kMaxRows / 2 && I <= kMaxRows / 2, "bad sizes");
+  MOE_REQUIRE(T >= 0 && H > 0 && I > 0, "bad sizes");
   if (T > moe::kDecodeTokens)
     return fail(MOE_ERR_UNSUPPORTED, "T=%lld: the layer for few tokens takes up to %d", (long long)T, moe::kDecodeTokens);
+  if (H > kDecodeMaxWidth || I > kDecodeMaxWidth)
+    return fail(MOE_ERR_UNSUPPORTED, "H=%lld or I=%lld exceeds %lld", (long long)H, (long long)I, (long long)kDecodeMaxWidth);
+  MOE_REQUIRE(H % 8 == 0 && I % 8 == 0, "H=%lld and I=%lld must be multiples of 8", (long long)H, (long long)I);
+  MOE_REQUIRE(I * H <= (long long)UINT32_MAX, "one expert's W13 must span under 4 GiB");
+  MOE_REQUIRE(T * H * 2 <= (long long)INT32_MAX && T * k * I * 2 <= (long long)INT32_MAX,
+              "x and the hidden rows must each span under 2 GiB");
+  return MOE_OK;
+}
+
+moe_status_t check_decode(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, moe_weights_t format, int32_t group) {
+  if (moe_status_t s = check_decode_sizes(T, H, I, E, k)) return s;
   int unit = 0;
   switch (format) {
     case MOE_WEIGHTS_BF16: unit = 8; break;
@@ -1248,8 +1262,6 @@ moe_status_t check_decode(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
                 (long long)H, (long long)I);
   const long long e_w = format == MOE_WEIGHTS_BF16 ? 4 : format == MOE_WEIGHTS_INT4 || format == MOE_WEIGHTS_MXFP4 ? 1 : 2;
   MOE_REQUIRE(I * H <= (long long)UINT32_MAX / e_w, "one expert's W13 must span under 4 GiB");
-  MOE_REQUIRE(T * H * 2 <= (long long)INT32_MAX && T * k * I * 2 <= (long long)INT32_MAX,
-              "x and the hidden rows must each span under 2 GiB");
   return MOE_OK;
 }
 
@@ -1258,7 +1270,7 @@ moe_status_t check_decode(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
 extern "C" {
 
 size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
-  if (check_decode(T, H, I, E, k, MOE_WEIGHTS_BF16, 0)) return 0;
+  if (check_decode_sizes(T, H, I, E, k)) return 0;
   return align256(moe::decode_plan_bytes()) + align256(T * k * I * 2);
 }
 
@@ -1314,7 +1326,7 @@ int64_t moe_adamw_state_elements(const int64_t* n, int64_t count) {
   if (count < 0 || (count > 0 && !n)) return -1;
   int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
-    if (n[i] < 0 || n[i] > (1ll << 40) || total > (1ll << 48)) return -1;
+    if (n[i] < 0 || n[i] > (1ll << 34) || total > (1ll << 48)) return -1;
     total += (n[i] + 127) & ~127ll;
   }
   return total;

@@ -8,6 +8,8 @@
 // sign, which order as integers do, with NaN above infinity: a row that holds one gets a NaN or infinite
 // scale and no other row notices.
 
+#include <algorithm>
+
 #include "launch.h"
 #include "rows_device.h"
 
@@ -52,7 +54,7 @@ __global__ __launch_bounds__(kQuantWaves<W> * 64) void quantize_rows_kernel(cons
   constexpr int kSlots = kWaves / W;
   __shared__ uint32_t red[kWaves];
   const int wave = threadIdx.x >> 6;
-  const long long t = (long long)blockIdx.x * kSlots + wave / W;
+  const long long t = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kSlots + wave / W;
   const int rl = (wave % W) * kWave + lane_id();
   const long long last = valid ? min(rows, (long long)max(*valid, 0)) : rows;
   const bool live = t < last;
@@ -104,7 +106,10 @@ struct QuantLauncher {
   template <int W, int C>
   hipError_t operator()() const {
     constexpr int kSlots = kQuantWaves<W> / W;
-    hipLaunchKernelGGL((quantize_rows_kernel<T, W, C>), dim3((unsigned)((p.rows + kSlots - 1) / kSlots)),
+    constexpr long long kMaxX = 1 << 20;   // a grid's axis has fewer than 2^32 threads
+    const long long blocks = (p.rows + kSlots - 1) / kSlots;
+    hipLaunchKernelGGL((quantize_rows_kernel<T, W, C>),
+                       dim3((unsigned)std::min(blocks, kMaxX), (unsigned)((blocks + kMaxX - 1) / kMaxX)),
                        dim3(kQuantWaves<W> * kWave), 0, stream, static_cast<const T*>(p.x), p.rows, p.valid, p.H,
                        static_cast<uint8_t*>(p.codes), p.scales);
     return hipGetLastError();

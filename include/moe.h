@@ -542,7 +542,7 @@ moe_status_t moe_forward_eightbit(const void* x, const float* router_logits, con
                                   void* stream);
 
 /* Bytes of device workspace moe_forward_decode needs (for every format); 0 for
- * invalid sizes or T > 16. */
+ * sizes that every format refuses. */
 size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k);
 
 /*
@@ -551,7 +551,8 @@ size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, 
  * weighted W2 h, in place of moe_forward's, moe_forward_eightbit's and
  * moe_forward_fourbit's five and more.
  *
- *   x            bf16 [T, H], T up to 16 (more is MOE_ERR_UNSUPPORTED).
+ *   x            bf16 [T, H], T up to 16, H and I up to 2^24 (more is
+ *                MOE_ERR_UNSUPPORTED).
  *   w13, w2      [E, 2I, H] and [E, H, I] in `format`, with their scales:
  *                MOE_WEIGHTS_BF16      none; H and I multiples of 8
  *                MOE_WEIGHTS_FP8_E4M3  f32 for each 128 x 128 block, as in moe_forward;
@@ -562,7 +563,8 @@ size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, 
  *                                      codes and scales of moe_quantize_fourbit with
  *                                      `group`; multiples of 32 and of group, at
  *                                      least 128 (less is MOE_ERR_UNSUPPORTED)
- *                One expert's W13 spans under 4 GiB.
+ *                One expert's W13 spans under 4 GiB, x and the routed rows of I
+ *                bf16 values under 2 GiB each.
  *   router_logits, num_valid_rows, renormalize: as for moe_route_topk.
  *   out          [T, H] of out_dtype (MOE_F32 or MOE_BF16); tokens without a valid row
  *                get exact zeros.
@@ -686,7 +688,8 @@ moe_status_t moe_unpermute_combine_dropout(const void* y, moe_dtype_t y_dtype, c
  * each operation, in the order of the formulas.
  */
 
-/* Elements of the state arrays of tensors with n[i] elements; -1 for invalid sizes. */
+/* Elements of the state arrays of tensors with n[i] elements, up to 2^34 each; -1
+ * for invalid sizes. */
 int64_t moe_adamw_state_elements(const int64_t* n, int64_t count);
 
 typedef struct {
