@@ -1,7 +1,9 @@
 """MI355X-native MoE expert layer: routing, sentinel-aware offsets, permute,
 grouped GEMMs with fused SiLU*up, and combine (and the layer's backward), its
-products on 4-bit weights at decode sizes, and the norm and dropout around it,
-as hand-written HIP for gfx950 behind the C ABI in ``include/moe.h``.
+products on 4-bit weights at decode sizes and on 8-bit integers at any, its form
+for up to 16 tokens in two kernels, the norm and dropout around it, and the
+AdamW step after its backward, as hand-written HIP for gfx950 behind the C ABI
+in ``include/moe.h``.
 
 ``ops`` holds torch-tensor wrappers (argument marshalling only); ``_lib``
 loads ``libmoe.so``; ``build`` compiles it.

@@ -20,12 +20,12 @@
 // that a token's sum over its experts ends in one place and needs no atomics: sums are joined through LDS in a
 // fixed order.
 //
-// First and second kernel, and the bytes of the weights that they read: bf16, 1 token, 4 experts of 2880 x 2880: 25.4
-// and 15.6 us, 133 and 66 MB (5.2 and 4.2 TB/s); e4m3, 8 tokens, 27 experts of 7168 x 2048: 138 and 91 us, about 790 and
-// 395 MB (5.7 and 4.3); mxfp4, 4 tokens, 15 experts of 2880 x 2880: 38 and 25.5 us, about 132 and 66 MB (3.5 and 2.6:
+// First and second kernel, and the bytes of the weights that they read: bf16, 1 token, 4 experts of 2880 x 2880: 24.5
+// and 15.5 us, 133 and 66 MB (5.4 and 4.3 TB/s); e4m3, 8 tokens, 30 experts of 7168 x 2048: 140 and 94 us, 870 and
+// 435 MB (6.2 and 4.6); mxfp4, 4 tokens, 15 experts of 2880 x 2880: 37.5 and 25.5 us, 129 and 65 MB (3.4 and 2.5:
 // rows of 1440 bytes, so that each 128 bytes are parts of two cache lines; with activations, scales and products
-// left out 33 and 18 us); int4 with groups of 32, 16 tokens, 68 experts of 2048 x 768: 45 and 25 us, about 134 and
-// 67 MB (3.0 and 2.7; 8 and 3 steps a row).
+// left out 33 and 18 us); int4 with groups of 32, 16 tokens, 71 experts of 2048 x 768: 41.5 and 25 us, 140 and 70 MB
+// (3.4 and 2.8; with those left out 33 and 19.5: 8 and 3 steps a row).
 
 #include <algorithm>
 #include <type_traits>
@@ -483,6 +483,9 @@ __device__ __forceinline__ void set_rows(Products<F, NM, NX>& p, const DecodePla
 // the maximum is one instruction; the lowest id of equal ones is the first lane that has the maximum, of the first
 // 64 experts that have it.  (Every workgroup routes every token: 16 of 128 experts, 8 each, were half of the first kernel's
 // instructions with route_token.)
+//
+// EPL: experts of a lane.  The rounds are a part of the first kernel that nothing hides: with 4 for 128 experts, 16
+// tokens and 8 each, it took 44.8 us for 41.6 with 2.
 template <int EPL>
 __device__ __forceinline__ void route(const UpArgs& a, int t, int* ids, float* weights) {
   const int lane = lane_id();
@@ -775,7 +778,9 @@ template <int F>
 hipError_t launch_both(const UpArgs& u, const DownArgs& d, hipStream_t stream) {
   hipError_t e;
   switch ((u.E + kWave - 1) / kWave) {
-    case 1: case 2: case 3: case 4: e = launch_up<F, 4>(u, stream); break;
+    case 1: e = launch_up<F, 1>(u, stream); break;
+    case 2: e = launch_up<F, 2>(u, stream); break;
+    case 3: case 4: e = launch_up<F, 4>(u, stream); break;
     default: e = launch_up<F, 16>(u, stream); break;
   }
   if (e != hipSuccess) return e;
