@@ -10,6 +10,8 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <utility>
+#include <vector>
 
 #include "decode_plan.h"
 #include "launch.h"
@@ -1362,6 +1364,20 @@ moe_status_t moe_adamw_step(void* const* params, const void* const* grads, const
     MOE_REQUIRE(params[i] && grads[i], "params[%lld] or grads[%lld] is null", (long long)i, (long long)i);
     MOE_REQUIRE(aligned16(params[i]) && aligned16(grads[i]), "params[%lld] and grads[%lld] must be 16-byte aligned",
                 (long long)i, (long long)i);
+  }
+  // a tensor listed twice would be updated by two workgroups at once
+  try {
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    spans.reserve((size_t)count);
+    for (int64_t i = 0; i < count; ++i) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(params[i]);
+      if (n[i] > 0) spans.emplace_back(at, at + (uintptr_t)n[i] * esize(p_dtype));
+    }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+      MOE_REQUIRE(spans[i - 1].second <= spans[i].first, "params overlap");
+  } catch (...) {
+    return fail(MOE_ERR_INVALID_ARG, "no host memory for %lld tensors", (long long)count);
   }
   moe::AdamwLaunch q{};
   q.count = count;

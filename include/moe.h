@@ -565,7 +565,8 @@ size_t moe_forward_decode_workspace(int64_t T, int64_t H, int64_t I, int32_t E, 
  *                                      least 128 (less is MOE_ERR_UNSUPPORTED)
  *                One expert's W13 spans under 4 GiB, x and the routed rows of I
  *                bf16 values under 2 GiB each.
- *   router_logits, num_valid_rows, renormalize: as for moe_route_topk.
+ *   router_logits, num_valid_rows, renormalize: as for moe_route_topk (a token with a NaN
+ *                among its logits may take other experts than there).
  *   out          [T, H] of out_dtype (MOE_F32 or MOE_BF16); tokens without a valid row
  *                get exact zeros.
  *   workspace    >= moe_forward_decode_workspace(...) bytes; no initialisation needed.
@@ -705,7 +706,8 @@ typedef struct {
  *
  *   params, grads  HOST arrays of `count` device pointers, n the HOST array of
  *                their elements (any number, also 0): p_dtype and g_dtype
- *                (MOE_F32 or MOE_BF16), 16-byte aligned.  No two params overlap.
+ *                (MOE_F32 or MOE_BF16), 16-byte aligned.  No two params overlap
+ *                (MOE_ERR_INVALID_ARG).
  *                The arrays are read before the call returns.
  *   state_dtype  MOE_F32 (m_scale, v_scale null) or MOE_FP8_E4M3.
  *   m, v         states as above, 16-byte aligned; m_scale and v_scale have

@@ -115,7 +115,7 @@ class Hyper(ctypes.Structure):
                 ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64)]
 
 
-def adamw(lib, n=(5, 0, 300), p=(0x10000,) * 3, g=(0x20000,) * 3, pd=BF16, gd=BF16, sd=F32, m=FAKE, ms=FAKE, v=FAKE,
+def adamw(lib, n=(5, 0, 300), p=(0x10000, 0x10000, 0x11000), g=(0x20000,) * 3, pd=BF16, gd=BF16, sd=F32, m=FAKE, ms=FAKE, v=FAKE,
           vs=FAKE, master=None, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.01, step=1, schedule=None, gs=None, rng=None,
           hyper=True):
     from grouped_gemm_histogram_amd import _lib
@@ -140,6 +140,8 @@ def test_adamw_refusals(lib):
     assert adamw(lib, pd=F32, master=FAKE) == INVALID          # f32 params are their own copy
     for name in ("m", "v", "master", "ms", "vs", "schedule", "gs", "rng"):
         assert adamw(lib, **{name: ODD}) == INVALID, name
+    assert adamw(lib, p=(0x10000, 0, 0x10000)) == INVALID and b"overlap" in lib.last_error()
+    assert adamw(lib, n=(8, 0, 300), p=(0x10010, 0, 0x10000 - 512)) == INVALID and b"overlap" in lib.last_error()
     assert adamw(lib, p=(0x10000, 0, None)) == INVALID and adamw(lib, g=(None, 0, 0x10000)) == INVALID
     assert adamw(lib, p=(0x10008, 0, 0x10000)) == INVALID
 
