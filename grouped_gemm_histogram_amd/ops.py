@@ -9,6 +9,7 @@ GPU, ``load()`` raises ImportError.
 
 from __future__ import annotations
 
+import array
 import ctypes
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -845,15 +846,15 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     dev, p_dtype, g_dtype = params[0].device, params[0].dtype, grads[0].dtype
     if not params[0].is_cuda or p_dtype not in _EL or g_dtype not in _EL:
         raise ValueError("params and grads must be GPU tensors of float32 or bfloat16")
-    sizes, total = [], 0
-    for i, (p, g) in enumerate(zip(params, grads)):
-        if p.dtype != p_dtype or g.dtype != g_dtype or p.device != dev or g.device != dev:
-            raise ValueError(f"params[{i}] or grads[{i}] has another dtype or device than the first")
+    sizes, total, index = [], 0, dev.index
+    for p, g in zip(params, grads):   # the host's time of a small step: whatever is slow stays out of the loop
+        if p.dtype is not p_dtype or g.dtype is not g_dtype or p.get_device() != index or g.get_device() != index:
+            raise ValueError(f"params[{len(sizes)}] or grads[{len(sizes)}] has another dtype or device than the first")
         if p.shape != g.shape or not p.is_contiguous() or not g.is_contiguous():
-            raise ValueError(f"params[{i}] and grads[{i}] must be contiguous and of one shape")
+            raise ValueError(f"params[{len(sizes)}] and grads[{len(sizes)}] must be contiguous and of one shape")
         n = p.numel()
         sizes.append(n)
-        total += (n + 127) // 128 * 128
+        total += (n + 127) & ~127
     small = state.m.dtype == torch.float8_e4m3fn
     _need(state.m, "state.m", (torch.float32, torch.float8_e4m3fn), (total,), dev)
     _need(state.v, "state.v", state.m.dtype, (total,), dev)
@@ -870,9 +871,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
         _need(schedule, "schedule", torch.float32, (3,), dev)
     if rng is not None:
         _need_rng(rng, dev)
-    pointers = ctypes.c_void_p * count
-    _run(load().adamw_step, dev, pointers(*[p.data_ptr() for p in params]), pointers(*[g.data_ptr() for g in grads]),
-         (ctypes.c_int64 * count)(*sizes), count, _DT[p_dtype], _DT[g_dtype], _DT[state.m.dtype], _a(state.m),
+    host = [array.array("q", a) for a in ([p.data_ptr() for p in params], [g.data_ptr() for g in grads], sizes)]
+    _run(load().adamw_step, dev, *[a.buffer_info()[0] for a in host], count, _DT[p_dtype], _DT[g_dtype], _DT[state.m.dtype], _a(state.m),
          _a(state.m_scale) if small else None, _a(state.v), _a(state.v_scale) if small else None, _a(state.master),
          ctypes.byref(MoeAdamw(lr, betas[0], betas[1], eps, weight_decay, step)), _a(schedule), _a(grad_scale),
          _a(rng))
