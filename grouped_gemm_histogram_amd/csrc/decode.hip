@@ -16,7 +16,7 @@
 //
 // The routing is recomputed by each workgroup of the first kernel (a wave a token at a time; a third launch or
 // a wait between workgroups would cost more) and left for the second one.  In the first kernel 1, 2, 4 or 8 waves share
-// K of 8 columns of two experts; in the second eight waves share all experts' K of 8 output columns, so
+// K of 8 columns of two experts; in the second 8 or 16 waves share all experts' K of 8 output columns, so
 // that a token's sum over its experts ends in one place and needs no atomics: sums are joined through LDS in a
 // fixed order.
 //
@@ -24,8 +24,8 @@
 // and 15.5 us, 133 and 66 MB (5.4 and 4.3 TB/s); e4m3, 8 tokens, 30 experts of 7168 x 2048: 140 and 94 us, 870 and
 // 435 MB (6.2 and 4.6); mxfp4, 4 tokens, 15 experts of 2880 x 2880: 37.5 and 25.5 us, 129 and 65 MB (3.4 and 2.5:
 // rows of 1440 bytes, so that each 128 bytes are parts of two cache lines; with activations, scales and products
-// left out 33 and 18 us); int4 with groups of 32, 16 tokens, 71 experts of 2048 x 768: 41.5 and 25 us, 140 and 70 MB
-// (3.4 and 2.8; with those left out 33 and 19.5: 8 and 3 steps a row).
+// left out 33 and 18 us); int4 with groups of 32, 16 tokens, 71 experts of 2048 x 768: 41.5 and 21 us, 140 and 70 MB
+// (3.4 and 3.3; 8 and 3 steps a row).
 
 #include <algorithm>
 #include <type_traits>
@@ -422,7 +422,8 @@ constexpr int kWaveLds = Products<F, NM, kMostXLds<F>>::kLds;
 
 constexpr int kWaves = 8;
 constexpr int kUpGroups = 512;     // workgroups of the first kernel: two on each of 256 CUs
-constexpr int kDownParts = 512;    // routed rows times shares of K that the second kernel's LDS holds
+template <int W>
+constexpr int kDownParts = 64 * W;    // routed rows times shares of K that the second kernel's LDS holds
 
 struct UpArgs {
   const uint8_t* x;       // [T, H] bf16
@@ -705,39 +706,39 @@ struct DownArgs {
   int out_bf16;
 };
 
-template <int F>
-__global__ __launch_bounds__(kWaves * kWave, 4) void decode_down_kernel(DownArgs a) {
+template <int F, int W>   // W: waves of a workgroup
+__global__ __launch_bounds__(W * kWave, 4) void decode_down_kernel(DownArgs a) {
   using T = FmtOf<F>;
   __shared__ DecodePlan plan;
-  __shared__ float part[kDownParts][8];
-  __shared__ __attribute__((aligned(16))) uint8_t lines[kWaves][kWaveLds<F, 1>];
-  static_assert(sizeof(plan) + sizeof(part) + sizeof(lines) <= 80 << 10, "two workgroups on a CU");
-  for (int i = threadIdx.x; i < (int)(sizeof(DecodePlan) / 16); i += kWaves * kWave)
+  __shared__ float part[kDownParts<W>][8];
+  __shared__ __attribute__((aligned(16))) uint8_t lines[W][kWaveLds<F, 1>];
+  static_assert(sizeof(plan) + sizeof(part) + sizeof(lines) <= (80 << 10) * (W / kWaves), "16 waves on a CU");
+  for (int i = threadIdx.x; i < (int)(sizeof(DecodePlan) / 16); i += W * kWave)
     reinterpret_cast<uint4*>(&plan)[i] = reinterpret_cast<const uint4*>(a.plan)[i];
   __syncthreads();
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 8;
   const int entries = __builtin_amdgcn_readfirstlane(plan.entries), pairs = (entries + 1) / 2;
-  // Shares of K: about four jobs a wave, at least one unit each.  shares * valid <= kDownParts: a pair
+  // Shares of K: about four jobs a wave, at least one unit each.  shares * valid <= 64 W: a pair
   // has up to 16 of the valid rows, all of them at most 256.
   const int units = (a.I / T::kVal * 16 + kStep - 1) / kStep;
-  const int shares = pairs ? max(min(4 * kWaves / pairs, units), 1) : 1;
+  const int shares = pairs ? max(min(4 * W / pairs, units), 1) : 1;
   const int all = pairs * shares;
   with_x_loads<F>(__builtin_amdgcn_readfirstlane(plan.most), [&](auto nx) {
     constexpr int NX = decltype(nx)::value;
     stream<F, 1, NX>(
-        lines[wave], all > wave ? (all - wave + kWaves - 1) / kWaves : 0, a.I / T::kVal * 16,
+        lines[wave], all > wave ? (all - wave + W - 1) / W : 0, a.I / T::kVal * 16,
         [&](int job, int& first, int& stride) {
-          const int unit = wave + job * kWaves;
+          const int unit = wave + job * W;
           first = unit - unit / shares * shares;
           stride = shares;
         },
         [&](int job, auto& p) {
-          const int at = 2 * ((wave + job * kWaves) / shares);
+          const int at = 2 * ((wave + job * W) / shares);
           set_rows(p, plan, at, n0, a.w, a.s, a.H, a.I, a.h, a.T * a.k, plan.rows);
         },
         [&](int job, const f32x4 (&acc)[1]) {
-          const int unit = wave + job * kWaves, pair = unit / shares, share = unit - pair * shares;
+          const int unit = wave + job * W, pair = unit / shares, share = unit - pair * shares;
           const int half = (lane >> 3) & 1, token0 = 4 * ((lane >> 4) & 1), at = 2 * pair + half;
           if (lane >> 5 != half || at >= entries) return;
           const int count = plan.count[at];
@@ -784,7 +785,14 @@ hipError_t launch_both(const UpArgs& u, const DownArgs& d, hipStream_t stream) {
     default: e = launch_up<F, 16>(u, stream); break;
   }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(decode_down_kernel<F>, dim3((d.H + 7) / 8), dim3(kWaves * kWave), 0, stream, d);
+  // Up to one workgroup a CU they have 16 waves, else 8, two on a CU.  The layer with 8 and with 16: H 2048, I 5632, 4
+  // tokens x 2 of 8 experts, int8 49.0 and 34.2 us, bf16 76.1 and 63.5; H 1024, I 2048, 16 x 4 of 32, bf16 88.2 and 78.2;
+  // slower only in int4 with more than four tokens of an expert (H = I = 1440, 16 x 4 of 32: 48.9 and 54.2).
+  const int blocks = (d.H + 7) / 8;
+  if (blocks <= kUpGroups / 2)
+    hipLaunchKernelGGL((decode_down_kernel<F, 2 * kWaves>), dim3(blocks), dim3(2 * kWaves * kWave), 0, stream, d);
+  else
+    hipLaunchKernelGGL((decode_down_kernel<F, kWaves>), dim3(blocks), dim3(kWaves * kWave), 0, stream, d);
   return hipGetLastError();
 }
 
