@@ -7,12 +7,13 @@
 //     p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 //
 // The step is bound by HBM: an element of bf16 parameters with bf16 gradients moves 22 bytes with
-// f32 states and 10 with 8-bit ones.  With f32 states, an f32 copy and f32 gradients 80 million elements take 498 us, 4.5
-// TB/s (a copy of as many bytes runs at 4.8 to 5.1); with 8-bit states and rounding by chance 100 million
-// elements take 229 us, 4.4 TB/s, with the VALU busy for most of it (94 instructions an element).  A lane therefore takes 8 consecutive elements, so that
-// every access is 8 or 16 bytes a lane and 16 lanes hold a block of 128 elements: the block's largest
-// value is a reduction over 16 lanes by rotations, without LDS.  A workgroup takes 2048 elements of one
-// tensor, found by a binary search over the first workgroups of up to 64 tensors that travel in the
+// f32 states and 10 with 8-bit ones.  With f32 states, an f32 copy and f32 gradients 75 million elements take
+// 500 us, 4.5 TB/s (a copy of as many bytes runs at 4.8 to 5.1); with 8-bit states and rounding by chance 100
+// million elements take 225 to 230 us, 4.4 TB/s, with the VALU busy for most of it (94 instructions an element).
+// A lane therefore takes 8 consecutive elements, so that every access is 8 or 16 bytes a lane and 16 lanes hold
+// a block of 128 elements: the block's largest value is a reduction over 16 lanes by rotations, without LDS.
+// A workgroup takes 2048 elements of one tensor, found by a binary search over the first workgroups of up to 64
+// tensors that travel in the
 // kernel's arguments: one launch for 64 tensors, nothing to copy or allocate.
 //
 // 8-bit states hold m and sqrt(v), not v: the root halves the exponents' range, so that e4m3's
@@ -80,7 +81,8 @@ template <bool kSigned, bool kFinite>
 __device__ __forceinline__ uint32_t e4m3_by_chance(float x, uint32_t piece) {
   const float a = fabsf(x);
   const bool small = a < 0.015625f;
-  const uint32_t b = __float_as_uint(small ? a + 0.015625f : a) + (piece << 4) + (small ? 8u - (968u << 20) : 8u - (960u << 20));
+  const uint32_t b = __float_as_uint(small ? a + 0.015625f : a) + (piece << 4) +
+                     (small ? 8u - (968u << 20) : 8u - (960u << 20));
   uint32_t code = min(b >> 20, 126u);
   if (kSigned) code |= (__float_as_uint(x) >> 24) & 0x80u;
   return kFinite || a < INFINITY ? code : 0x7fu;
