@@ -59,7 +59,7 @@ struct FmtOf {
 constexpr int kStep = 128;
 
 // One step's weights, scales and activations of a lane.  NX: loads of activations, which hold kXTokens * NX tokens of each
-// expert; NX = 8 (4 bits only): of all eight tokens, in the MFMA's layout.
+// expert; NX = 8 (4 bits only): four of each 64-byte piece's channels, which go through LDS one piece after the other.
 template <int F, int NM, int NX>
 struct Step {
   using T = FmtOf<F>;
@@ -125,15 +125,17 @@ template <int F, int NM, int NX>
 struct Products {
   using T = FmtOf<F>;
   using S = Step<F, NM, NX>;
-  static constexpr bool kDirect = NX == 8;
+  static constexpr bool kHalves = NX == 8;
+  static constexpr int kXLoads = kHalves ? 4 : NX;                    // that LDS holds
+  static constexpr int kXRow = kHalves ? T::kXRow / 2 : T::kXRow;     // bytes of a token there
   // LDS of a wave: weights, activations, scales
-  static constexpr int kW = NM * 2048, kX = kDirect ? 0 : NX * 1024, kLds = kW + kX + 64 * T::kScale;
+  static constexpr int kW = NM * 2048, kX = kXLoads * 1024, kLds = kW + kX + 64 * T::kScale;
   const uint8_t* w[NM][2];    // uniform: the two experts' first weight rows
   uint32_t w_bytes;           // of an expert's rows of a matrix, below kPast
   uint32_t w_off;             // the loads' row and byte
   const uint8_t* x;           // uniform
   uint32_t x_bytes;           // below kPast
-  uint32_t x_off[kDirect ? 1 : NX];   // the loads' rows and bytes; kPast where an expert has no such token
+  uint32_t x_off[kXLoads];    // the loads' rows and bytes; kPast where an expert has no such token
   const uint8_t* s;           // the scales that the lane loads: of its row, matrix and piece
   int row_bytes;              // of a weight row
 
@@ -144,9 +146,9 @@ struct Products {
   }
   // the bytes of a step that the lane loads of its weight row and of its token row
   static __device__ __forceinline__ int w_lane() { return 16 * (lane_id() & 7); }
-  static __device__ __forceinline__ int x_load() { return 16 * lane_id() & (T::kXRow - 1); }
+  static __device__ __forceinline__ int x_load() { return 16 * lane_id() & (kXRow - 1); }
   // load i's token in lanes of this lane's place, and which of the two experts' it is
-  static __device__ __forceinline__ int x_row(int i) { return i * 2 * T::kXTokens + lane_id() / (T::kXRow / 16); }
+  static __device__ __forceinline__ int x_row(int i) { return i * (1024 / kXRow) + lane_id() / (kXRow / 16); }
   // the lane's scales: of matrix m, piece p
   static __device__ __forceinline__ int s_matrix() { return NM == 2 ? lane_id() >> 5 : 0; }
   static __device__ __forceinline__ int s_piece() { return F == kE4m3 ? 0 : (lane_id() >> 4) & 1; }
@@ -163,15 +165,11 @@ struct Products {
     const uint32_t wo = w_off | past | (w_lane() < left ? 0u : kPast);
     const auto rows = buffer(x, x_bytes);
     const int x_at = at / 16 * T::kXBytes;
-    if constexpr (kDirect) {
 #pragma unroll
-      for (int i = 0; i < 2 * T::kX; ++i)
-        b.x[i] = load16(rows, (x_off[0] | past | (64 * i + x_lane() < x_left ? 0u : kPast)) + 64 * i, x_at);
-    } else {
-      const uint32_t end = past | (x_load() < x_left ? 0u : kPast);
+    for (int h = 0; h < NX / kXLoads; ++h) {
+      const uint32_t end = past | (kXRow * h + x_load() < x_left ? 0u : kPast);
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
-        b.x[i] = load16(rows, x_off[i] | end, x_at);
+      for (int i = 0; i < kXLoads; ++i) b.x[kXLoads * h + i] = load16(rows, (x_off[i] | end) + kXRow * h, x_at);
     }
 #pragma unroll
     for (int m = 0; m < NM; ++m)
@@ -205,7 +203,12 @@ struct Products {
   // Loaded lines to LDS, and from there in the MFMA's layout.  16-byte chunk j of weight row r is kept at j ^ (r % 8),
   // of a token's row at j ^ (token + 8 * expert), within 128 bytes where a row has no more: neither side has bank conflicts.
   static __device__ __forceinline__ int x_chunk(int row, int chunk) {
-    return T::kXRow * row + 16 * (chunk ^ (T::kXRow == 128 ? row >> 1 & 7 : (row >> 1 & 7) | (row & 1) << 3));
+    return kXRow * row + 16 * (chunk ^ (kXRow == 128 ? row >> 1 & 7 : (row >> 1 & 7) | (row & 1) << 3));
+  }
+  static __device__ __forceinline__ void put_x(uint8_t* lds, const S& b, int h) {
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i)
+      *reinterpret_cast<uint4*>(lds + kW + x_chunk(x_row(i), x_load() / 16)) = b.x[kXLoads * h + i];
   }
   static __device__ __forceinline__ void put(uint8_t* lds, const S& b) {
     const int lane = lane_id(), r = lane >> 3;
@@ -214,10 +217,7 @@ struct Products {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         *reinterpret_cast<uint4*>(lds + 2048 * m + 1024 * i + 128 * r + 16 * ((lane & 7) ^ r)) = b.w[m][i];
-    if constexpr (!kDirect) {
-#pragma unroll
-      for (int i = 0; i < NX; ++i) *reinterpret_cast<uint4*>(lds + kW + x_chunk(x_row(i), x_load() / 16)) = b.x[i];
-    }
+    put_x(lds, b, 0);
     if constexpr (T::kScale > 0) {
       uint32_t* to = reinterpret_cast<uint32_t*>(lds + kW + kX + T::kScale * (4 * (lane & 15) + (lane >> 4)));
 #pragma unroll
@@ -229,14 +229,10 @@ struct Products {
     const uint4 v = *reinterpret_cast<const uint4*>(lds + 2048 * m + 128 * c + 16 * ((4 * p + g) ^ (c & 7)));
     d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
   }
-  // the activations of the step's MFMA i; tokens past the loaded ones repeat the last
-  static __device__ __forceinline__ bf16x8 get_x(const uint8_t* lds, const S& b, int i) {
-    if constexpr (kDirect) {
-      return as_bf16x8(b.x[i]);
-    } else {
-      const int c = lane_id() & 15, row = 2 * min(c & 7, T::kXTokens * NX - 1) + (c >> 3);
-      return as_bf16x8(*reinterpret_cast<const uint4*>(lds + kW + x_chunk(row, 4 * i + x_lane() / 16)));
-    }
+  // the activations of the step's MFMA i (of those in LDS); tokens past the loaded ones repeat the last
+  static __device__ __forceinline__ bf16x8 get_x(const uint8_t* lds, int i) {
+    const int c = lane_id() & 15, row = 2 * min(c & 7, kXLoads * (512 / kXRow) - 1) + (c >> 3);
+    return as_bf16x8(*reinterpret_cast<const uint4*>(lds + kW + x_chunk(row, 4 * i + x_lane() / 16)));
   }
   static __device__ __forceinline__ void get_scales(const uint8_t* lds, int m, int p, uint32_t (&d)[T::kGroups]) {
     const uint32_t* from = reinterpret_cast<const uint32_t*>(lds + kW + kX + T::kScale * (4 * (lane_id() & 15) + 2 * m + p));
@@ -252,12 +248,13 @@ struct Products {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       if (T::kFour) __builtin_amdgcn_sched_barrier(0);   // one piece's operands at a time
+      if (kHalves && p == 1) put_x(lds, b, 1);   // behind the first piece's reads: a wave's LDS accesses stay in order
       uint32_t d[NM][4], s[NM][T::kGroups];
 #pragma unroll
       for (int m = 0; m < NM; ++m) get_weights(lds, m, p, d[m]);
       bf16x8 x[T::kX];
 #pragma unroll
-      for (int q = 0; q < T::kX; ++q) x[q] = get_x(lds, b, T::kX * p + q);
+      for (int q = 0; q < T::kX; ++q) x[q] = get_x(lds, kHalves ? q : T::kX * p + q);
       if constexpr (T::kFour) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) get_scales(lds, m, p, s[m]);
@@ -471,12 +468,8 @@ __device__ __forceinline__ void set_rows(Products<F, NM, NX>& p, const DecodePla
     const int entry = at + half;
     return entry < plan.entries && token < plan.count[entry] ? (uint32_t)rows[entry][token] * (uint32_t)K * 2 + byte : kPast;
   };
-  if constexpr (P::kDirect) {
-    p.x_off[0] = row_of(c >> 3, c & 7, P::x_lane());
-  } else {
 #pragma unroll
-    for (int i = 0; i < NX; ++i) p.x_off[i] = row_of(P::x_row(i) & 1, P::x_row(i) >> 1, P::x_load());
-  }
+  for (int i = 0; i < P::kXLoads; ++i) p.x_off[i] = row_of(P::x_row(i) & 1, P::x_row(i) >> 1, P::x_load());
 }
 
 // Top-k routing of one token by a wave, with the ids and weights of route_device.h's route_token: k rounds of a
