@@ -166,18 +166,18 @@ __device__ __forceinline__ void store8(void* p, long long at, int n, const float
 }
 
 // u = sqrt(v), rounded to nearest.  Goldschmidt's iteration on a 1-ulp reciprocal root and Markstein's last
-// correction by the exact residual take 10 instructions for sqrtf's 16; they need v's residual, 2^-48 v, to be
-// a normal number, so a wave with a smaller v above zero (or an infinite one) takes sqrtf.
+// correction by the residual take 10 instructions for sqrtf's 16.  The residual v - s^2 is a multiple of 2^-48 v and
+// has to be exact: from v = 2^-96 on it is, as a subnormal number in part.  A wave with a smaller v above zero, or with
+// one that is negative, infinite or NaN, takes sqrtf: the clamp below would make numbers of a root that is NaN.
 __device__ __forceinline__ void roots(const float (&v)[kPer], float (&u)[kPer]) {
 #pragma clang fp contract(off)
-  uint32_t least = 0xffffffffu;
-  float most = 0.0f;
+  uint32_t least = 0xffffffffu, most = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    least = min(least, __float_as_uint(v[j]) - 1u);   // zeros (and negative values, whose root is NaN) pass
-    most = fmaxf(most, v[j]);
+    least = min(least, __float_as_uint(v[j]) - 1u);   // zeros pass
+    most = max(most, __float_as_uint(v[j]));          // with a sign, or infinite, or NaN: from 0x7f800000 on
   }
-  if (__any(least < 0x0f800000u - 1u || !(most < INFINITY))) {   // 2^-96
+  if (__any(least < 0x0f800000u - 1u || most >= 0x7f800000u)) {   // 2^-96
 #pragma unroll
     for (int j = 0; j < kPer; ++j) u[j] = sqrtf(v[j]);
     return;
