@@ -798,7 +798,8 @@ def adamw_starts(params: Sequence[torch.Tensor]):
 
 
 def adamw_init(params: Sequence[torch.Tensor], bits: int = 32, master: bool = False) -> AdamWState:
-    """States at the start of a run: zeros, and with ``master`` the params' values in float32."""
+    """States at the start of a run: zeros, and with ``master`` the params' values in float32.  Plain tensors, also of
+    params that require gradients."""
     if bits not in (8, 32):
         raise ValueError(f"bits must be 8 or 32, not {bits}")
     if not params:
@@ -813,7 +814,7 @@ def adamw_init(params: Sequence[torch.Tensor], bits: int = 32, master: bool = Fa
     if master:
         state.master = new(n, torch.float32)
         for p, at in zip(params, starts):
-            state.master[at:at + p.numel()] = p.reshape(-1)
+            state.master[at:at + p.numel()] = p.detach().reshape(-1)
     return state
 
 
