@@ -840,6 +840,9 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     step, for a step captured in a graph.  ``rng``: GPU int64 (or uint64) [2], seed and offset: 8-bit
     states, and bf16 params without master, round by chance in place of to nearest; advance rng[1] by
     adamw_counters(params) between calls.
+
+    The version counters of params and states go up, so autograd refuses a backward pass through params that were
+    saved before the step (a graph's replay does not raise them, as with torch's own operations).
     """
     count = len(params)
     if count == 0 or len(grads) != count:
@@ -877,3 +880,9 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
          _a(state.m_scale) if small else None, _a(state.v), _a(state.v_scale) if small else None, _a(state.master),
          ctypes.byref(MoeAdamw(lr, betas[0], betas[1], eps, weight_decay, step)), _a(schedule), _a(grad_scale),
          _a(rng))
+    written = [*params, state.m, state.v]
+    if small:
+        written += (state.m_scale, state.v_scale)
+    if state.master is not None:
+        written.append(state.master)
+    torch.autograd.graph.increment_version(written)
