@@ -728,8 +728,12 @@ typedef struct {
  *                of offset + i/8, 2, 0).  A call uses offset + [0, elements/8): advance
  *                offset by that much between calls.
  *
- * A gradient that is infinite or NaN makes its element NaN, with 8-bit states
- * its 128 elements.  One launch for 64 tensors.
+ * A gradient (times grad_scale) that is NaN makes its element NaN, in params and
+ * states, and no other.  An infinite one makes its param NaN, and so, with 8-bit states,
+ * the params of its 128 elements from the next step on: their scale is infinite.  One of
+ * 2^64 or more has an infinite square: from this step on its param moves by the
+ * decay only; with 8-bit states, from the next step on, so do its 128 elements, but
+ * it and those whose v was zero become NaN.  One launch for 64 tensors.
  */
 moe_status_t moe_adamw_step(void* const* params, const void* const* grads, const int64_t* n, int64_t count,
                             moe_dtype_t p_dtype, moe_dtype_t g_dtype, moe_dtype_t state_dtype, void* m, float* m_scale,
