@@ -8,11 +8,12 @@
 // operands in registers, where all of these codes are exact, and scales multiply f32 sums (mxfp4's
 // powers of two the operand).
 //
-// The bytes of the routed experts' weights bound it: every weight is read once, in whole cache lines of 8 rows a load.
+// The bytes of the routed experts' weights bound it; they are read in whole cache lines of 8 rows a load.
 // One v_mfma_f32_16x16x32_bf16 has 8 rows of each of two experts and up to 8 tokens of each: of its 16 x 16
 // results the two 8 x 8 blocks where expert and token belong together are used.  So a wave works on 8 columns at
-// a time, which splits the columns of small layers over more workgroups; an expert of more than 8
-// tokens is listed twice.
+// a time, which splits the columns of small layers over more workgroups.  An expert of up to 8 tokens is listed and
+// its weights are loaded once; one of more is listed twice, in general in two pairs, whose waves each load its weights.
+// With an odd number of entries the last one is both halves of its pair (the same wave loads the same lines twice).
 //
 // The routing is recomputed by each workgroup of the first kernel (a wave a token at a time; a third launch or
 // a wait between workgroups would cost more) and left for the second one.  In the first kernel 1, 2, 4 or 8 waves share
@@ -778,9 +779,11 @@ hipError_t launch_both(const UpArgs& u, const DownArgs& d, hipStream_t stream) {
     default: e = launch_up<F, 16>(u, stream); break;
   }
   if (e != hipSuccess) return e;
-  // Up to one workgroup a CU they have 16 waves, else 8, two on a CU.  The layer with 8 and with 16: H 2048, I 5632, 4
-  // tokens x 2 of 8 experts, int8 49.0 and 34.2 us, bf16 76.1 and 63.5; H 1024, I 2048, 16 x 4 of 32, bf16 88.2 and 78.2;
-  // slower only in int4 with more than four tokens of an expert (H = I = 1440, 16 x 4 of 32: 48.9 and 54.2).
+  // Up to one workgroup a CU they have 16 waves, else 8, two on a CU.  The layer with 8 and with 16, in us: H 1024, I 2048,
+  // 4 of 32 experts, 16 tokens, bf16 85.6 and 68.9, int4 46.5 and 42.7; H 2048, I 5632, 2 of 8, 4 tokens, bf16 70.6 and 63.6,
+  // int8 47.8 and 42.9; H = I = 1440, 4 of 32, 16 tokens, 8 of them with one expert, int4 54.3 and 53.1, int8 65.5 and 60.1.  Over
+  // H from 512 to 2048, 1 to 16 tokens and all formats 16 lose at most 4% (one token in bf16, 20.1 and 20.9), and up
+  // to 2% in 4 bits where experts have up to four tokens (H 1024, I 1440, 4 of 32, 16 tokens, mxfp4 37.7 and 38.6).
   const int blocks = (d.H + 7) / 8;
   if (blocks <= kUpGroups / 2)
     hipLaunchKernelGGL((decode_down_kernel<F, 2 * kWaves>), dim3(blocks), dim3(2 * kWaves * kWave), 0, stream, d);
