@@ -241,15 +241,25 @@ struct Products {
     for (int i = 0; i < T::kGroups; ++i) d[i] = from[i];
   }
 
+  // Between LDS accesses of lanes of the wave that depend on each other.  The hardware keeps a wave's in order; this holds
+  // the compiler to it, which sees the accesses of one lane only.  No instruction.
+  static __device__ __forceinline__ void keep_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
   static __device__ __forceinline__ void use(uint8_t* lds, const S& b, f32x4 (&acc)[NM]) {
     f32x4 part[NM];   // e4m3: the block's sum
 #pragma unroll
     for (int m = 0; m < NM; ++m) part[m] = f32x4{0, 0, 0, 0};
+    keep_order();
     put(lds, b);
+    keep_order();
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       if (T::kFour) __builtin_amdgcn_sched_barrier(0);   // one piece's operands at a time
-      if (kHalves && p == 1) put_x(lds, b, 1);   // behind the first piece's reads: a wave's LDS accesses stay in order
+      if (kHalves && p == 1) {   // behind the first piece's reads
+        keep_order();
+        put_x(lds, b, 1);
+        keep_order();
+      }
       uint32_t d[NM][4], s[NM][T::kGroups];
 #pragma unroll
       for (int m = 0; m < NM; ++m) get_weights(lds, m, p, d[m]);
