@@ -9,7 +9,9 @@
 // The step is bound by HBM: an element of bf16 parameters with bf16 gradients moves 22 bytes with
 // f32 states and 10 with 8-bit ones.  With f32 states, an f32 copy and f32 gradients 75 million elements take
 // 500 us, 4.5 TB/s (a copy of as many bytes runs at 4.8 to 5.1); with 8-bit states and rounding by chance 100
-// million elements take 225 to 230 us, 4.4 TB/s, with the VALU busy for most of it (94 instructions an element).
+// million elements take 224 to 231 us one call after the other, 4.4 TB/s, with the VALU busy for most of it (94
+// instructions an element).  By the profiler's durations, with its pauses between the calls, 499 to 507 and 225 to 266 us
+// (least and median of 15).
 // A lane therefore takes 8 consecutive elements, so that every access is 8 or 16 bytes a lane and 16 lanes hold
 // a block of 128 elements: the block's largest value is a reduction over 16 lanes by rotations, without LDS.
 // A workgroup takes 2048 elements of one tensor, found by a binary search over the first workgroups of up to 64

@@ -190,8 +190,9 @@ constexpr int kMaxExperts = 1024;
 #define MOE_DECODE_NARROW_ROWS_PER_EXPERT 2
 #endif
 // 8-bit integers: 8192 x 8192 x 8192 in 494 us, 2224 TOPS (a library's product of them 455 us, 2418), 16384 x 5760 x
-// 2880 over 32 experts with SiLU * up 380 us, 1430 TOPS: of 23 slices a tile more is start and end (with twice the
-// slices 1870).  Others were slower there: 256 x 256 with two stages 392 us, 128 x 256 428, 256 x 192 462,
+// 2880 over 32 experts with SiLU * up 366 us one call after the other, 1490 TOPS, and by the profiler's durations 372 to
+// 398 (least and median of 15): of 23 slices a tile more is start and end (with twice the slices 1870).  Others were
+// slower there, beside 385 for this tile in the same run: 256 x 256 with two stages 392 us, 128 x 256 428, 256 x 192 462,
 // 128 x 128, two on a CU, 448 (with even segments of 1024 rows x 2048 x 2048 it takes 45 us for 60, but with a
 // routing's segments of about 512 rows x 4096 x 14336 382 us for 313).
 #ifndef MOE_TILE_I8

@@ -513,6 +513,7 @@ moe_status_t moe_quantize_rows_eightbit(const void* x, moe_dtype_t x_dtype, int6
  *   C            [M_rows, N_out] of c_dtype (MOE_F32 or MOE_BF16), rows of whole 16 bytes;
  *                rows from offsets[E] on are written as exact zeros.
  *
+ * The sum is scaled by a_scales first, which has to stay in f32's range, then by b_scales.
  * Everything else (offsets, epi, the 4 GiB limits, errors) is as in moe_grouped_gemm.
  * With E = 1 it is the plain product.
  */
